@@ -416,6 +416,79 @@ kda_status kda_debug_k1_records(kda_ctx *ctx, const kda_plan *plan, const void *
                                 const void *v, const float *g, const float *beta,
                                 const int32_t *cu_seqlens_dev, void *records, hipStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Gated delta rule: the recurrence with one log-decay per token and head,
+ *   S_t = (I - beta_t k_t k_t^T) exp(g_t) S_{t-1} + beta_t k_t v_t^T,
+ *   o_t = scale * S_t^T q_t,
+ * over the same packed layouts and states, with g: fp32 [Tt, H] (g <= 0
+ * expected; -inf forgets the state). Products are taken with the state and the
+ * other computed operands as pairs of bf16 numbers, so an fp32 state is within
+ * about 1e-5 of the exact one relative to its norm; bf16 outputs and states
+ * are rounded once.
+ * ------------------------------------------------------------------------- */
+
+/* Build the plan of a packed batch for kda_gated_delta_prefill. mode OFF runs
+ * every sequence as one unit per head. ON cuts every sequence longer than
+ * seg_chunks chunks of 32 tokens into even segments of at most that length;
+ * seg_chunks = 0 picks the length. AUTO segments when that is predicted to be
+ * faster (few heads, long sequences). A segment's end state from zero and its
+ * transfer matrix are formed first, the states between segments merged from
+ * them, and all segments then run side by side; the results differ from the
+ * unsegmented ones by fp32-level rounding. Errors and the upload of the
+ * tables are as in kda_plan_prefill; H is at most 131072. The plan is only
+ * accepted by kda_gated_delta_prefill, and the inspection calls. */
+kda_status kda_plan_gated_delta(kda_ctx *ctx, const int32_t *cu_seqlens_host, int32_t n_seqs, int32_t H,
+                                int32_t dk, int32_t dv, kda_cp_mode mode, int32_t seg_chunks, kda_plan **out);
+
+/* The same for an explicit compute-unit count, host only (not executable). */
+kda_status kda_plan_gated_delta_host(int32_t n_cus, const int32_t *cu_seqlens_host, int32_t n_seqs, int32_t H,
+                                     int32_t dk, int32_t dv, kda_cp_mode mode, int32_t seg_chunks, kda_plan **out);
+
+/* Run the prefill on `stream`. Arguments are those of kda_prefill_ex, with
+ *   g         : fp32 [Tt, H] (device, 4-byte aligned)
+ *   workspace : kda_plan_workspace_bytes(plan) bytes of device memory (16-byte
+ *               aligned, or NULL when that is 0), owned by the caller and used
+ *               until the call's work on `stream` is done; it may overlap no
+ *               other argument. Two calls that may run at the same time, or
+ *               graphs that may be replayed at the same time, need one each.
+ * The call allocates nothing and synchronises nothing. final_state may equal
+ * initial_state. Results are bitwise reproducible. */
+kda_status kda_gated_delta_prefill(kda_ctx *ctx, const kda_plan *plan, const kda_prefill_opts *opts, const void *q,
+                                   const void *k, const void *v, const float *g, const void *beta,
+                                   const int32_t *cu_seqlens_dev, float scale, const void *initial_state,
+                                   void *final_state, void *out, void *workspace, size_t workspace_bytes,
+                                   hipStream_t stream);
+
+/* The argument checks of kda_gated_delta_prefill (addresses only; no GPU). */
+kda_status kda_gated_delta_prefill_validate(const kda_plan *plan, const kda_prefill_opts *opts, const void *q,
+                                            const void *k, const void *v, const float *g, const void *beta,
+                                            const int32_t *cu_seqlens_dev, float scale, const void *initial_state,
+                                            const void *final_state, const void *out, const void *workspace,
+                                            size_t workspace_bytes);
+
+/* Decode: each of n_seqs sequences receives n_tokens new tokens, in order, and
+ * its state is advanced in place (n_tokens = 1 for plain decoding; more for
+ * drafted tokens or a short continuation, with the state read and written
+ * once; a call with n tokens gives the bits of n calls with one).
+ *   q, k    : bf16 [n_seqs, n_tokens, qk_heads, 128]
+ *   v, out  : bf16 [n_seqs, n_tokens, H, 128]
+ *   g, beta : fp32 [n_seqs, n_tokens, H]
+ *   state   : fp32 [n_slots, H, 128, 128]; slots (device int32 [n_seqs], or
+ *             NULL with n_slots = n_seqs) as in kda_decode_slots: a slot
+ *             outside the pool skips its sequence, and no two may be equal
+ * Alignment, aliasing and errors as in kda_decode_slots. One launch, no
+ * workspace. */
+kda_status kda_gated_delta_decode(kda_ctx *ctx, int32_t n_seqs, int32_t n_tokens, int32_t H, int32_t qk_heads,
+                                  int32_t dk, int32_t dv, const void *q, const void *k, const void *v, const float *g,
+                                  const float *beta, float scale, float *state, int32_t n_slots, const int32_t *slots,
+                                  void *out, hipStream_t stream);
+
+/* The argument checks of kda_gated_delta_decode (addresses only; no GPU). */
+kda_status kda_gated_delta_decode_validate(int32_t n_seqs, int32_t n_tokens, int32_t H, int32_t qk_heads, int32_t dk,
+                                           int32_t dv, const void *q, const void *k, const void *v, const float *g,
+                                           const float *beta, float scale, const float *state, int32_t n_slots,
+                                           const int32_t *slots, const void *out);
+
 /* Per-kernel timing of kda_prefill and kda_decode calls on this context: while enabled,
  * every call records HIP events around each of its launches on its stream.
  * kda_get_timing waits for all recorded events, and returns, per kernel name

@@ -9,6 +9,8 @@ every entry point raises.
     o, s = kda.prefill(q, k, v, g, beta, cu_seqlens=cu, initial_state=s0,
                        output_final_state=True, use_intracard_cp="auto")
     o_t = kda.decode(q_t, k_t, v_t, g_t, beta_t, s)   # one token each, s in place
+    o, s = kda.gated_delta_prefill(q, k, v, g1, beta, cu_seqlens=cu, output_final_state=True)
+    o_t = kda.gated_delta_decode(q_t, k_t, v_t, g1_t, beta_t, s)   # g1: one decay per head
 
 The interface follows the FLA-compatible prefill of "feat(kda/sm90): FlashKDA
 prefill port + intracard-CP prefill" (cuLA pull request #103, description:
@@ -26,6 +28,7 @@ import os
 import threading
 
 __all__ = ["prefill", "decode", "plan", "plan_host", "plan_segments", "Plan", "Context", "context",
+           "gated_delta_prefill", "gated_delta_decode", "plan_gated_delta", "plan_gated_delta_host",
            "KDAError", "lib", "LIB_PATH", "CP_OFF", "CP_ON", "CP_AUTO"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -115,6 +118,16 @@ def lib():
                 "kda_decode_slots": (ctypes.c_int, [P, I32, I32, I32, I32, I32, P, P, P, P, P, F32, P, I32, P, P, P]),
                 "kda_decode_slots_validate": (ctypes.c_int, [I32, I32, I32, I32, I32, P, P, P, P, P, F32, P, I32, P,
                                                              P]),
+                "kda_plan_gated_delta": (ctypes.c_int, [P, P, I32, I32, I32, I32, ctypes.c_int, I32, PP]),
+                "kda_plan_gated_delta_host": (ctypes.c_int, [I32, P, I32, I32, I32, I32, ctypes.c_int, I32, PP]),
+                "kda_gated_delta_prefill": (ctypes.c_int, [P, P, ctypes.POINTER(PrefillOpts), P, P, P, P, P, P, F32,
+                                                           P, P, P, P, ctypes.c_size_t, P]),
+                "kda_gated_delta_prefill_validate": (ctypes.c_int, [P, ctypes.POINTER(PrefillOpts), P, P, P, P, P, P,
+                                                                    F32, P, P, P, P, ctypes.c_size_t]),
+                "kda_gated_delta_decode": (ctypes.c_int, [P, I32, I32, I32, I32, I32, I32, P, P, P, P, P, F32, P, I32,
+                                                          P, P, P]),
+                "kda_gated_delta_decode_validate": (ctypes.c_int, [I32, I32, I32, I32, I32, I32, P, P, P, P, P, F32,
+                                                                   P, I32, P, P]),
                 "kda_set_timing": (ctypes.c_int, [P, ctypes.c_int]),
                 "kda_get_timing": (I32, [P, ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(ctypes.c_double),
                                          ctypes.POINTER(I32), I32]),
@@ -218,6 +231,7 @@ class Plan:
         self.device = device
         self._cu_dev = None
         self._shape = None
+        self._ws_bytes = None
 
     def __del__(self):
         try:
@@ -238,6 +252,12 @@ class Plan:
             i = self.info()
             self._shape = (i["H"], i["total_tokens"], i["n_seqs"])
         return self._shape
+
+    def workspace_bytes(self):
+        """Bytes of workspace a call with this plan uses (cached)."""
+        if self._ws_bytes is None:
+            self._ws_bytes = lib().kda_plan_workspace_bytes(self.handle)
+        return self._ws_bytes
 
     def units(self):
         n = self.info()["n_units"]
@@ -313,11 +333,11 @@ _PLAN_CACHE_MAX = 64
 _captured_plans = []
 
 
-def _cached_plan(cu_host, H, mode, device):
-    key = (device, tuple(cu_host), H, mode)
+def _cached_plan(cu_host, H, mode, device, make=plan):
+    key = (device, tuple(cu_host), H, mode, make)
     p = _plan_cache.get(key)
     if p is None:
-        p = plan(cu_host, H, mode, device="cuda:%d" % device)
+        p = make(cu_host, H, mode, device="cuda:%d" % device)
         _plan_cache[key] = p
         if len(_plan_cache) > _PLAN_CACHE_MAX:
             _plan_cache.popitem(last=False)
@@ -494,3 +514,169 @@ def decode(q, k, v, g, beta, state, scale=1.0, out=None, slots=None):
     _check(lib().kda_decode(ctx.handle, N, H, Hk, D, D, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
                             float(scale), _ptr(state), _ptr(out), ctypes.c_void_p(stream)), "kda_decode")
     return out.view(shape)
+
+
+# ---------------------------------------------------------------------------
+# gated delta rule
+# ---------------------------------------------------------------------------
+def plan_gated_delta(cu_seqlens, H, use_intracard_cp="auto", seg_chunks=0, device=None):
+    """Executable plan of a gated delta rule prefill. use_intracard_cp=True
+    with seg_chunks cuts sequences into segments of at most that many chunks
+    of 32 tokens (0: chosen)."""
+    ctx = context(device)
+    arr, n = _cu_array(cu_seqlens)
+    h = ctypes.c_void_p()
+    _check(lib().kda_plan_gated_delta(ctx.handle, arr, n, int(H), D, D, _cp_mode(use_intracard_cp), int(seg_chunks),
+                                      ctypes.byref(h)), "kda_plan_gated_delta")
+    return Plan(h, cu_seqlens, ctx.device)
+
+
+def plan_gated_delta_host(cu_seqlens, H, n_cus, use_intracard_cp="auto", seg_chunks=0):
+    """The same for an explicit CU count (inspection; no GPU needed)."""
+    arr, n = _cu_array(cu_seqlens)
+    h = ctypes.c_void_p()
+    _check(lib().kda_plan_gated_delta_host(int(n_cus), arr, n, int(H), D, D, _cp_mode(use_intracard_cp),
+                                           int(seg_chunks), ctypes.byref(h)), "kda_plan_gated_delta_host")
+    return Plan(h, cu_seqlens)
+
+
+def _need(name, t, dtype, shape, device):
+    """Raise unless t is a contiguous tensor of this type, shape and device."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device or device.type != "cuda":
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s, a CUDA device (got %s %s on %s, strides "
+                         "%s)" % (name, dtype, tuple(shape), device, t.dtype, tuple(t.shape), t.device, t.stride()))
+
+
+def _stream(device):
+    import torch
+    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+def gated_delta_prefill(q, k, v, g, beta, cu_seqlens=None, initial_state=None, output_final_state=False,
+                        use_intracard_cp="auto", scale=1.0, final_state=None, out=None, plan=None,
+                        cu_seqlens_host=None, state_dtype=None):
+    """Gated delta rule forward prefill: one log-decay per token and head.
+
+    q, k, v: bf16 [Tt, H, 128] packed, or [B, T, H, 128] (B equal-length
+    sequences when cu_seqlens is None); g: fp32 log-decay [Tt, H] (or
+    [B, T, H]); beta: fp32 or bf16, same shape. Grouped value heads,
+    cu_seqlens, the states, scale, out and the returned (o, final_state or
+    None) are as in prefill. use_intracard_cp: "auto" cuts long sequences with
+    few heads into segments (equal up to fp32-level rounding), False never
+    does. plan: from plan_gated_delta. The workspace of a segmented plan comes
+    from torch's allocator, on the current stream.
+    """
+    import torch
+    if q.dim() == 4:
+        B, T = q.shape[0], q.shape[1]
+        if cu_seqlens is None and cu_seqlens_host is None:
+            cu_seqlens_host = [i * T for i in range(B + 1)]
+        elif B != 1:
+            raise ValueError("4-D inputs with cu_seqlens must have batch size 1")
+        flat = lambda x: x.reshape(B * T, *x.shape[2:])
+        if out is not None and not out.is_contiguous():
+            raise ValueError("out must be contiguous")
+        o, s = gated_delta_prefill(flat(q), flat(k), flat(v), flat(g), flat(beta), cu_seqlens, initial_state,
+                                   output_final_state, use_intracard_cp, scale, final_state,
+                                   None if out is None else flat(out), plan, cu_seqlens_host, state_dtype)
+        return o.view(v.shape), s
+    if q.dim() != 3 or q.shape[-1] != D or v.dim() != 3:
+        raise ValueError("q must be [Tt, H, 128] or [B, T, H, 128], got %s" % (tuple(q.shape),))
+    Tt, Hk, H, dev = q.shape[0], q.shape[1], v.shape[1], q.device
+    if Hk < 1 or H < 1 or H % Hk:
+        raise ValueError("v has %d heads, not a multiple of the %d q/k heads" % (H, Hk))
+    beta16 = beta.dtype == torch.bfloat16
+    _need("q", q, torch.bfloat16, (Tt, Hk, D), dev)
+    _need("k", k, torch.bfloat16, (Tt, Hk, D), dev)
+    _need("v", v, torch.bfloat16, (Tt, H, D), dev)
+    _need("g", g, torch.float32, (Tt, H), dev)
+    _need("beta", beta, torch.bfloat16 if beta16 else torch.float32, (Tt, H), dev)
+    if cu_seqlens_host is None:
+        if cu_seqlens is None:
+            cu_seqlens_host = [0, Tt]
+        elif isinstance(cu_seqlens, (list, tuple)):
+            cu_seqlens_host = cu_seqlens
+        else:
+            cu_seqlens_host = cu_seqlens.tolist()  # host copy for the planner (synchronises)
+    cu_seqlens_host = [int(x) for x in cu_seqlens_host]
+    N = len(cu_seqlens_host) - 1
+    # the library sizes every buffer from the plan, so the table must describe
+    # exactly the packed tokens the tensors hold
+    if (N < 1 or cu_seqlens_host[0] != 0 or cu_seqlens_host[-1] != Tt
+            or any(b < a for a, b in zip(cu_seqlens_host, cu_seqlens_host[1:]))):
+        raise ValueError("cu_seqlens must start at 0, never decrease and end at the %d packed tokens (got %s)"
+                         % (Tt, cu_seqlens_host[:8]))
+    if plan is None:
+        plan = _cached_plan(cu_seqlens_host, H, _cp_mode(use_intracard_cp), dev.index, plan_gated_delta)
+    elif plan.device != dev.index or plan.shape() != (H, Tt, N) or plan.cu_host != cu_seqlens_host:
+        raise ValueError("the plan was built for device %s, H=%d, %d tokens, %d sequences (cu_seqlens %s...); the call "
+                         "has device %s, H=%d, %d tokens, %d sequences"
+                         % (plan.device, *plan.shape(), plan.cu_host[:4], dev.index, H, Tt, N))
+    if cu_seqlens is None or isinstance(cu_seqlens, (list, tuple)):
+        cu_dev = plan.cu_device()
+    else:
+        cu_dev = cu_seqlens
+        _need("cu_seqlens", cu_dev, torch.int32, (N + 1,), dev)
+    if state_dtype is None:
+        given = initial_state if initial_state is not None else final_state
+        state_dtype = given.dtype if given is not None else torch.float32
+    if state_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("states must be fp32 or bf16, got %s" % (state_dtype,))
+    if initial_state is not None:
+        _need("initial_state", initial_state, state_dtype, (N, H, D, D), dev)
+    if final_state is not None:
+        _need("final_state", final_state, state_dtype, (N, H, D, D), dev)
+    elif output_final_state:
+        final_state = torch.empty(N, H, D, D, dtype=state_dtype, device=dev)
+    if out is None:
+        out = torch.empty_like(v)
+    else:
+        _need("out", out, torch.bfloat16, (Tt, H, D), dev)
+    n_ws = plan.workspace_bytes()
+    ws = torch.empty(n_ws, dtype=torch.uint8, device=dev) if n_ws else None
+    if torch.cuda.is_current_stream_capturing() and not any(p is plan for p in _captured_plans):
+        _captured_plans.append(plan)
+    opts = PrefillOpts(Hk, int(beta16), int(state_dtype == torch.bfloat16))
+    _check(lib().kda_gated_delta_prefill(context(dev).handle, plan.handle, ctypes.byref(opts), _ptr(q), _ptr(k),
+                                         _ptr(v), _ptr(g), _ptr(beta), _ptr(cu_dev), float(scale),
+                                         _ptr(initial_state), _ptr(final_state), _ptr(out), _ptr(ws), n_ws,
+                                         _stream(dev)), "kda_gated_delta_prefill")
+    return out, final_state
+
+
+def gated_delta_decode(q, k, v, g, beta, state, scale=1.0, out=None, slots=None):
+    """Gated delta rule decode: new tokens per sequence, state advanced in place.
+
+    q, k, v: bf16 [N, H, 128] (one token each) or [N, T, H, 128] (T tokens
+    each, in order); g: fp32 log-decay [N, H] or [N, T, H]; beta: fp32, same
+    shape; state: fp32 [N, H, 128, 128], overwritten. q and k may have fewer
+    heads than v (grouped value heads, as in prefill). With slots (int32 CUDA
+    tensor [N]), state is a pool [n_slots, H, 128, 128] and sequence n uses
+    slot slots[n]; a slot outside the pool skips that sequence (zero output),
+    and no two sequences may share one. Returns o, shaped like v.
+    """
+    import torch
+    if q.dim() not in (3, 4) or v.dim() != q.dim() or q.shape[-1] != D:
+        raise ValueError("q must be [N, H, 128] or [N, T, H, 128] (and v alike), got %s" % (tuple(q.shape),))
+    rows, Hk, H, dev = q.shape[:-2], q.shape[-2], v.shape[-2], q.device
+    N = rows[0]
+    if Hk < 1 or H < 1 or H % Hk:
+        raise ValueError("v has %d heads, not a multiple of the %d q/k heads" % (H, Hk))
+    _need("q", q, torch.bfloat16, (*rows, Hk, D), dev)
+    _need("k", k, torch.bfloat16, (*rows, Hk, D), dev)
+    _need("v", v, torch.bfloat16, (*rows, H, D), dev)
+    _need("g", g, torch.float32, (*rows, H), dev)
+    _need("beta", beta, torch.float32, (*rows, H), dev)
+    n_slots = N
+    if slots is not None:
+        _need("slots", slots, torch.int32, (N,), dev)
+        n_slots = state.shape[0]
+    _need("state", state, torch.float32, (n_slots, H, D, D), dev)
+    if out is None:
+        out = torch.empty_like(v)
+    else:
+        _need("out", out, torch.bfloat16, v.shape, dev)
+    _check(lib().kda_gated_delta_decode(context(dev).handle, N, rows[1] if len(rows) == 2 else 1, H, Hk, D, D,
+                                        _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), float(scale), _ptr(state),
+                                        n_slots, _ptr(slots), _ptr(out), _stream(dev)), "kda_gated_delta_decode")
+    return out

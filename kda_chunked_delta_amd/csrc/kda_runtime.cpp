@@ -22,16 +22,17 @@
 #include <unordered_map>
 #include <vector>
 
-#include "kda_launch.h"
 #include "kda_decode_launch.h"
+#include "kda_internal.h"
 
 using namespace kda;
 
 namespace {
-
 thread_local std::string g_last_error;
+}
 
-kda_status fail(kda_status st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
+namespace kda {
+
 kda_status fail(kda_status st, const char* fmt, ...) {
     char buf[512];
     va_list ap;
@@ -46,7 +47,15 @@ kda_status hip_fail(hipError_t e, const char* what) {
     return fail(KDA_ERR_HIP, "%s failed: %s", what, hipGetErrorString(e));
 }
 
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    if (!a || !b || na == 0 || nb == 0) return false;
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return x < y + nb && y < x + na;
+}
+
+}  // namespace kda
+
+namespace {
 
 // Per-device addresses of the static scratch of kda_prefill_noalloc, each
 // looked up once, with its device current.
@@ -185,44 +194,6 @@ double simulate_fused_us(std::vector<int> work, int n_cus, const PlannerConsts& 
 }
 
 }  // namespace
-
-// ---------------------------------------------------------------------------
-// plan
-// ---------------------------------------------------------------------------
-struct kda_plan {
-    kda_plan_info info{};
-    std::vector<int32_t> cu;            // host copy of cu_seqlens
-    std::vector<ChunkDesc> chunks;      // K1 items (global chunk order)
-    std::vector<UnitDesc> units;        // K2 units, launch order
-    std::vector<MergeDesc> merges;      // CP merge items
-    std::vector<UnitDesc> fixups;       // warm-start segments, as rerun from their carry
-    std::vector<UnitDesc> cp_units;     // warm-start CP: the segmented fallback's K2 units
-    std::vector<UnitDesc> alt_units;    // split plans: the batch unsplit (the exact path)
-    std::vector<UnitDesc> k1_units;     // segmented pipeline: K1 with the B summaries, one per K2 unit
-    std::vector<MergeSeg> merge_segs;   // segmented pipeline: one merge workgroup row per segment
-    // workspace layout (byte offsets into the arena)
-    size_t off_rec = 0, off_b = 0, off_m = 0, off_mlive = 0, off_carry = 0;
-    size_t off_spec_states = 0, off_spec_flags = 0, off_gate = 0;
-    // device copy of the tables
-    int device = -1;
-    void* dev_tables = nullptr;
-    size_t dev_off_chunks = 0, dev_off_units = 0, dev_off_merges = 0, dev_off_fixups = 0;
-    size_t dev_off_cp_units = 0, dev_off_alt_units = 0, dev_off_k1_units = 0, dev_off_merge_segs = 0;
-    // Speculation feedback, outside graph capture: a speculative call (the
-    // first, then every 64th) copies its outcome (split plans: the speculation
-    // flags; warm-start CP: the gate) into pinned host memory and records an
-    // event; a later call
-    // that finds the copy complete and a failure in it turns speculation off
-    // for this plan, which then runs its exact path (unsplit serial, or the
-    // segmented pipeline ungated). Results are the same bits either way.
-    mutable std::mutex spec_mu;
-    mutable int32_t* spec_host = nullptr;
-    mutable size_t spec_words = 0;
-    mutable hipEvent_t spec_event = nullptr;
-    mutable bool spec_pending = false;
-    mutable bool spec_off = false;
-    mutable uint64_t spec_calls = 0;  // the outcome is copied on the first call and every 64th
-};
 
 namespace {
 
@@ -668,68 +639,7 @@ kda_status upload_plan(kda_plan* p, int device) {
     return KDA_OK;
 }
 
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-    if (!a || !b || na == 0 || nb == 0) return false;
-    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-    return x < y + nb && y < x + na;
-}
-
 }  // namespace
-
-// ---------------------------------------------------------------------------
-// context and arena
-// ---------------------------------------------------------------------------
-struct Arena {
-    void* ptr = nullptr;
-    size_t bytes = 0;
-    // A call captured into a graph bakes this address into the graph, which
-    // may be replayed at any time after: such memory is never freed before
-    // kda_destroy (growing or evicting the arena retires it instead).
-    bool captured = false;
-};
-
-struct TimedLaunch {
-    const char* name;
-    hipEvent_t beg, end;
-};
-
-struct kda_ctx {
-    int device = 0;
-    int n_cus = 0;
-    hipDeviceProp_t prop{};
-    std::mutex mu;
-    std::unordered_map<hipStream_t, Arena> arenas;
-    std::vector<void*> retired;  // arena memory that served a graph capture, freed in kda_destroy
-    void* scratch = nullptr;     // this device's copy of the static scratch (kda_prefill_noalloc)
-    bool poison = false;
-    bool timing = false;
-    std::vector<TimedLaunch> events;  // pool, reused across calls
-    int n_timed = 0;
-};
-
-static const size_t kMaxArenas = 16;
-static const int kMaxTimedLaunches = 4096;
-
-// Run `launch` on `stream`; while the context's timing is on, bracket it with
-// a pair of HIP events from the context's pool (ctx->mu held by the caller).
-template <class F>
-static hipError_t timed_launch(kda_ctx* ctx, hipStream_t stream, const char* name, F&& launch) {
-    if (!ctx->timing) return launch();
-    if (ctx->n_timed >= kMaxTimedLaunches) return launch();  // log full: run untimed
-    if ((int)ctx->events.size() <= ctx->n_timed) {
-        TimedLaunch t{name, nullptr, nullptr};
-        hipError_t ee = hipEventCreate(&t.beg);
-        if (ee == hipSuccess) ee = hipEventCreate(&t.end);
-        if (ee != hipSuccess) return ee;
-        ctx->events.push_back(t);
-    }
-    TimedLaunch& t = ctx->events[ctx->n_timed++];
-    t.name = name;
-    hipError_t ee = hipEventRecord(t.beg, stream);
-    if (ee == hipSuccess) ee = launch();
-    if (ee == hipSuccess) ee = hipEventRecord(t.end, stream);
-    return ee;
-}
 
 extern "C" {
 
@@ -905,6 +815,7 @@ kda_status kda_prefill_ex_validate(const kda_plan* p, const kda_prefill_opts* op
                                    const void* v, const float* g, const void* beta, const int32_t* cu_dev,
                                    float scale, const void* s0, const void* sT, const void* out) {
     if (!p) return fail(KDA_ERR_INVALID, "kda_prefill: plan is NULL");
+    if (p->gated) return fail(KDA_ERR_INVALID, "kda_prefill: the plan is a gated delta rule plan");
     const kda_plan_info& in = p->info;
     const int32_t qk_heads = (opts && opts->qk_heads > 0) ? opts->qk_heads : in.H;
     const bool beta16 = opts && opts->beta_bf16, state16 = opts && opts->state_bf16;
