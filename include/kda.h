@@ -489,6 +489,102 @@ kda_status kda_gated_delta_decode_validate(int32_t n_seqs, int32_t n_tokens, int
                                            const float *beta, float scale, const float *state, int32_t n_slots,
                                            const int32_t *slots, const void *out);
 
+/* ---------------------------------------------------------------------------
+ * Pages of a state pool, and beam search over it. A page is one slot of a pool
+ * of states [n_pages, H, 128, 128] (of kda_decode_slots or
+ * kda_gated_delta_decode); with several layers it is that slot of each. All
+ * calls work on device tables, enqueue on `stream`, allocate nothing,
+ * synchronise nothing and can be captured into graphs. `used` is uint8
+ * [n_pages], nonzero for a page in use. Entries outside [0, n_pages) in a
+ * table (-1 for a padded one) are skipped.
+ * ------------------------------------------------------------------------- */
+typedef struct {
+    void *base;           /* page p of layer l: base + l * layer_stride + p * page_bytes; 16-byte aligned */
+    int64_t layer_stride; /* bytes, a multiple of 16, at least n_pages * page_bytes; ignored with one layer */
+    int64_t page_bytes;   /* a multiple of 16 */
+    int32_t n_layers;     /* >= 1 */
+    int32_t n_pages;
+} kda_pool;
+
+/* Copy page src[i] to page dst[i] for i < n <= 1024, as if every source were
+ * read before any destination is written (a swap, a rotation or any other
+ * rearrangement in place). Of pairs with one destination the last counts. */
+kda_status kda_pool_copy(kda_ctx *ctx, const kda_pool *pool, const int32_t *src, const int32_t *dst, int32_t n,
+                         hipStream_t stream);
+kda_status kda_pool_copy_validate(const kda_pool *pool, const int32_t *src, const int32_t *dst, int32_t n);
+
+/* Fork: dst[i] becomes a free page that is marked used and gets a copy of page
+ * src[i]. The requests with a used source take the lowest free pages in the
+ * order of i (one page may be forked several times). A request gets dst[i] =
+ * -1 and changes nothing when its source is not a used page or no page is
+ * left. n <= 8192. used, src and dst may not overlap. */
+kda_status kda_pool_fork(kda_ctx *ctx, const kda_pool *pool, uint8_t *used, const int32_t *src, int32_t *dst,
+                         int32_t n, hipStream_t stream);
+kda_status kda_pool_fork_validate(const kda_pool *pool, const uint8_t *used, const int32_t *src, const int32_t *dst,
+                                  int32_t n);
+
+/* Mark pages[0 .. n) free (free and repeated ones included). */
+kda_status kda_pool_free(kda_ctx *ctx, int32_t n_pages, uint8_t *used, const int32_t *pages, int32_t n,
+                         hipStream_t stream);
+kda_status kda_pool_free_validate(int32_t n_pages, const uint8_t *used, const int32_t *pages, int32_t n);
+
+/* Compact: the used pages are moved to the first pages of the pool. Pages that
+ * lie there already stay; the others take the holes, in page order.
+ * new_pages [n_pages] gets each used page's new index (-1 for a free page),
+ * n_live [1] the number of used pages, used is rewritten, and table [n_table]
+ * (may be NULL with n_table = 0) has its entries replaced by the new ones (-1
+ * for an entry that names no used page). */
+kda_status kda_pool_compact(kda_ctx *ctx, const kda_pool *pool, uint8_t *used, int32_t *table, int32_t n_table,
+                            int32_t *new_pages, int32_t *n_live, hipStream_t stream);
+kda_status kda_pool_compact_validate(const kda_pool *pool, const uint8_t *used, const int32_t *table, int32_t n_table,
+                                     const int32_t *new_pages, const int32_t *n_live);
+
+/* Reorder a beam batch's states after a selection: afterwards page
+ * new_slots[b, w] holds what page slots[b, parents[b, w]] held. slots, parents
+ * and new_slots are int32 [batch, beams], beams <= 64, the pages of slots
+ * distinct. Only states that several beams continue are copied: the first
+ * beam that continues a parent keeps its page, the others take, in order, the
+ * pages of the parents that no beam continues. A beam whose parent is outside
+ * [0, beams) gets one of the pages left over, with undefined contents. new_slots may
+ * not overlap slots or parents. */
+kda_status kda_beam_reorder(kda_ctx *ctx, const kda_pool *pool, const int32_t *slots, const int32_t *parents,
+                            int32_t *new_slots, int32_t batch, int32_t beams, hipStream_t stream);
+kda_status kda_beam_reorder_validate(const kda_pool *pool, const int32_t *slots, const int32_t *parents,
+                                     const int32_t *new_slots, int32_t batch, int32_t beams);
+
+typedef enum { KDA_FP32 = 0, KDA_BF16 = 1, KDA_FP16 = 2 } kda_dtype;
+
+/* Beam search's selection. For beam w of batch entry b, candidate token t has
+ * the value scores[b, w] + log_softmax(logits[b, w])[t]. The n candidates of
+ * highest value over the beams and the vocabulary are selected per batch entry, in the
+ * order of value; the candidates of one beam go by logit, then by the lower t,
+ * equal values of two beams by the lower w.
+ *   logits  : [batch * beams] rows of vocab elements, row_stride elements apart
+ *             (aligned to an element)
+ *   scores  : fp32 [batch, beams]
+ *   finished: uint8 [batch, beams] or NULL: a nonzero beam has the single
+ *             candidate eos, at scores[b, w]; its other tokens count as -inf
+ *   eos     : the end token, or -1 for none (then finished and out_finished
+ *             are NULL)
+ *   out_scores fp32, out_parents and out_tokens int32 [batch, n];
+ *   out_finished uint8 [batch, n]: the parent was finished or the token is eos
+ * NaN logits and scores count as -inf; a row without a logit above -inf has
+ * all candidates at -inf; +inf logits share their row's probability. Values
+ * are compared in fp64, with the log-sum-exp within 2e-7 (equal rows tie exactly). beams <= 64,
+ * n <= 64 and n <= beams * vocab. The workspace (16-byte aligned, of
+ * kda_beam_select_workspace_bytes) is the caller's until the call's work is
+ * done; calls that may run at the same time need one each. */
+size_t kda_beam_select_workspace_bytes(int32_t batch, int32_t beams, int32_t vocab, int32_t n);
+kda_status kda_beam_select(kda_ctx *ctx, int32_t batch, int32_t beams, int32_t vocab, int32_t n, const void *logits,
+                           kda_dtype dtype, int64_t row_stride, const float *scores, const uint8_t *finished,
+                           int32_t eos, float *out_scores, int32_t *out_parents, int32_t *out_tokens,
+                           uint8_t *out_finished, void *workspace, size_t workspace_bytes, hipStream_t stream);
+kda_status kda_beam_select_validate(int32_t batch, int32_t beams, int32_t vocab, int32_t n, const void *logits,
+                                    kda_dtype dtype, int64_t row_stride, const float *scores, const uint8_t *finished,
+                                    int32_t eos, const float *out_scores, const int32_t *out_parents,
+                                    const int32_t *out_tokens, const uint8_t *out_finished, const void *workspace,
+                                    size_t workspace_bytes);
+
 /* Per-kernel timing of kda_prefill and kda_decode calls on this context: while enabled,
  * every call records HIP events around each of its launches on its stream.
  * kda_get_timing waits for all recorded events, and returns, per kernel name

@@ -29,6 +29,7 @@ import threading
 
 __all__ = ["prefill", "decode", "plan", "plan_host", "plan_segments", "Plan", "Context", "context",
            "gated_delta_prefill", "gated_delta_decode", "plan_gated_delta", "plan_gated_delta_host",
+           "beam_select", "beam_reorder", "pool_copy", "pool_fork", "pool_free", "pool_compact",
            "KDAError", "lib", "LIB_PATH", "CP_OFF", "CP_ON", "CP_AUTO"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -66,6 +67,11 @@ class PlanInfo(ctypes.Structure):
 
 class PrefillOpts(ctypes.Structure):
     _fields_ = [("qk_heads", ctypes.c_int32), ("beta_bf16", ctypes.c_int32), ("state_bf16", ctypes.c_int32)]
+
+
+class Pool(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("layer_stride", ctypes.c_int64), ("page_bytes", ctypes.c_int64),
+                ("n_layers", ctypes.c_int32), ("n_pages", ctypes.c_int32)]
 
 
 class UnitInfo(ctypes.Structure):
@@ -128,6 +134,21 @@ def lib():
                                                           P, P, P]),
                 "kda_gated_delta_decode_validate": (ctypes.c_int, [I32, I32, I32, I32, I32, I32, P, P, P, P, P, F32,
                                                                    P, I32, P, P]),
+                "kda_pool_copy": (ctypes.c_int, [P, ctypes.POINTER(Pool), P, P, I32, P]),
+                "kda_pool_copy_validate": (ctypes.c_int, [ctypes.POINTER(Pool), P, P, I32]),
+                "kda_pool_fork": (ctypes.c_int, [P, ctypes.POINTER(Pool), P, P, P, I32, P]),
+                "kda_pool_fork_validate": (ctypes.c_int, [ctypes.POINTER(Pool), P, P, P, I32]),
+                "kda_pool_free": (ctypes.c_int, [P, I32, P, P, I32, P]),
+                "kda_pool_free_validate": (ctypes.c_int, [I32, P, P, I32]),
+                "kda_pool_compact": (ctypes.c_int, [P, ctypes.POINTER(Pool), P, P, I32, P, P, P]),
+                "kda_pool_compact_validate": (ctypes.c_int, [ctypes.POINTER(Pool), P, P, I32, P, P]),
+                "kda_beam_reorder": (ctypes.c_int, [P, ctypes.POINTER(Pool), P, P, P, I32, I32, P]),
+                "kda_beam_reorder_validate": (ctypes.c_int, [ctypes.POINTER(Pool), P, P, P, I32, I32]),
+                "kda_beam_select_workspace_bytes": (ctypes.c_size_t, [I32, I32, I32, I32]),
+                "kda_beam_select": (ctypes.c_int, [P, I32, I32, I32, I32, P, ctypes.c_int, I64, P, P, I32, P, P, P, P,
+                                                   P, ctypes.c_size_t, P]),
+                "kda_beam_select_validate": (ctypes.c_int, [I32, I32, I32, I32, P, ctypes.c_int, I64, P, P, I32, P, P,
+                                                            P, P, P, ctypes.c_size_t]),
                 "kda_set_timing": (ctypes.c_int, [P, ctypes.c_int]),
                 "kda_get_timing": (I32, [P, ctypes.POINTER(ctypes.c_char_p), ctypes.POINTER(ctypes.c_double),
                                          ctypes.POINTER(I32), I32]),
@@ -680,3 +701,162 @@ def gated_delta_decode(q, k, v, g, beta, state, scale=1.0, out=None, slots=None)
                                         _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), float(scale), _ptr(state),
                                         n_slots, _ptr(slots), _ptr(out), _stream(dev)), "kda_gated_delta_decode")
     return out
+
+
+# ---------------------------------------------------------------------------
+# pages of a state pool, and beam search over it
+# ---------------------------------------------------------------------------
+def _pool(pool, page_dim):
+    """The library's view of a pool tensor with pages along page_dim (layers before it)."""
+    if pool.dim() <= page_dim or page_dim not in (0, 1):
+        raise ValueError("pool must be [pages, ...] (page_dim=0) or [layers, pages, ...] (page_dim=1), got %s"
+                         % (tuple(pool.shape),))
+    if pool.device.type != "cuda" or not pool.numel():
+        raise ValueError("pool must be a non-empty CUDA tensor, got %s on %s" % (tuple(pool.shape), pool.device))
+    page = pool[0] if page_dim == 0 else pool[0, 0]
+    n_pages = pool.shape[page_dim]
+    size = pool.element_size()
+    n = page.numel()
+    if not page.is_contiguous() or (n_pages > 1 and pool.stride(page_dim) != n):
+        raise ValueError("the pages of a pool must be contiguous and back to back (strides %s)" % (pool.stride(),))
+    layers = pool.shape[0] if page_dim else 1
+    return Pool(pool.data_ptr(), pool.stride(0) * size if layers > 1 else 0, n * size, layers, n_pages)
+
+
+def pool_copy(pool, src, dst, page_dim=0):
+    """Copy page src[i] of a state pool to page dst[i], as if every source were
+    read before any destination is written (swaps and rotations included).
+
+    pool: [pages, ...], or [layers, pages, ...] with page_dim=1; any type, a
+    page being a multiple of 16 bytes. src, dst: int32 CUDA tensors of up to
+    1024 entries; pairs with an entry outside the pool (-1) are skipped, of
+    pairs with one destination the last counts. In place, returns pool.
+    """
+    import torch
+    view, dev = _pool(pool, page_dim), pool.device
+    n = src.numel()
+    _need("src", src, torch.int32, (n,), dev)
+    _need("dst", dst, torch.int32, (n,), dev)
+    _check(lib().kda_pool_copy(context(dev).handle, ctypes.byref(view), _ptr(src), _ptr(dst), n, _stream(dev)),
+           "kda_pool_copy")
+    return pool
+
+
+def pool_fork(pool, used, src, page_dim=0):
+    """Fork pages of a state pool: each source gets a copy in a free page.
+
+    pool as in pool_copy; used: bool [pages], updated in place; src: int32
+    CUDA tensor of up to 8192 entries (repeats allowed). The requests whose
+    source is in use take the lowest free pages in order. Returns the new pages
+    (int32, like src): -1 where the source is no used page or none was free.
+    """
+    import torch
+    view, dev = _pool(pool, page_dim), pool.device
+    n = src.numel()
+    _need("src", src, torch.int32, (n,), dev)
+    _need("used", used, torch.bool, (view.n_pages,), dev)
+    dst = torch.empty_like(src)
+    _check(lib().kda_pool_fork(context(dev).handle, ctypes.byref(view), _ptr(used), _ptr(src), _ptr(dst), n,
+                               _stream(dev)), "kda_pool_fork")
+    return dst
+
+
+def pool_free(used, pages):
+    """Mark pages (int32 CUDA tensor) free in used (bool [n_pages], in place, returned).
+    Entries outside the pool are skipped; free and repeated ones are harmless."""
+    import torch
+    n, dev = pages.numel(), used.device
+    _need("used", used, torch.bool, (used.numel(),), dev)
+    _need("pages", pages, torch.int32, (n,), dev)
+    _check(lib().kda_pool_free(context(dev).handle, used.numel(), _ptr(used), _ptr(pages), n, _stream(dev)),
+           "kda_pool_free")
+    return used
+
+
+def pool_compact(pool, used, table=None, page_dim=0):
+    """Move the used pages of a state pool to its first pages.
+
+    pool and used as in pool_fork, both updated in place; table: int32 CUDA
+    tensor of pages (a slot table of any shape), whose entries are replaced in
+    place by the new pages (-1 where they name no used page). Pages that lie in
+    front already stay. Returns (new_pages, n_live): int32 [pages], each used
+    page's new index or -1, and int32 [1], the number of used pages.
+    """
+    import torch
+    view, dev = _pool(pool, page_dim), pool.device
+    _need("used", used, torch.bool, (view.n_pages,), dev)
+    if table is not None:
+        _need("table", table, torch.int32, table.shape, dev)
+    new_pages = torch.empty(view.n_pages, dtype=torch.int32, device=dev)
+    n_live = torch.empty(1, dtype=torch.int32, device=dev)
+    _check(lib().kda_pool_compact(context(dev).handle, ctypes.byref(view), _ptr(used), _ptr(table),
+                                  0 if table is None else table.numel(), _ptr(new_pages), _ptr(n_live), _stream(dev)),
+           "kda_pool_compact")
+    return new_pages, n_live
+
+
+def beam_reorder(pool, slots, parents, page_dim=0):
+    """Let a beam batch's states follow their parents.
+
+    pool as in pool_copy; slots: int32 [B, W], the (distinct) pages of the
+    beams; parents: int32 [B, W], the beam of the same batch entry that each
+    continues (the second result of beam_select). W <= 64. Returns the new
+    slots: page new[b, w] holds what page slots[b, parents[b, w]] held. Only
+    states that several beams continue are copied, into pages whose beam ends.
+    """
+    import torch
+    view, dev = _pool(pool, page_dim), pool.device
+    if slots.dim() != 2:
+        raise ValueError("slots must be [batch, beams], got %s" % (tuple(slots.shape),))
+    _need("slots", slots, torch.int32, slots.shape, dev)
+    _need("parents", parents, torch.int32, slots.shape, dev)
+    new = torch.empty_like(slots)
+    _check(lib().kda_beam_reorder(context(dev).handle, ctypes.byref(view), _ptr(slots), _ptr(parents), _ptr(new),
+                                  slots.shape[0], slots.shape[1], _stream(dev)), "kda_beam_reorder")
+    return new
+
+
+def beam_select(logits, scores, n=None, finished=None, eos=None):
+    """Beam search's selection: the n best of beams x vocabulary per batch entry.
+
+    logits: [B, W, V] fp32, bf16 or fp16, rows of V contiguous elements at one
+    even distance (a slice of a padded vocabulary is fine); scores: fp32
+    [B, W] running log-probabilities. Candidate (w, t) has the value
+    scores[w] + log_softmax(logits[w])[t]; the candidates of one beam go by
+    logit, then by the lower t, equal values of two beams by the lower w.
+    n: candidates per batch entry (default W; at most 64). finished: bool
+    [B, W], needs eos: such a beam has the single candidate eos, at its own
+    score. NaN counts as -inf. Returns (scores [B, n] fp32, parents [B, n]
+    int32, tokens [B, n] int32, finished [B, n] bool, or None without eos).
+    """
+    import torch
+    if logits.dim() != 3 or logits.device.type != "cuda":
+        raise ValueError("logits must be a CUDA tensor [batch, beams, vocab], got %s on %s"
+                         % (tuple(logits.shape), logits.device))
+    B, W, V = logits.shape
+    dev = logits.device
+    dtype = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}.get(logits.dtype)
+    if dtype is None:
+        raise ValueError("logits must be fp32, bf16 or fp16, got %s" % logits.dtype)
+    row = logits.stride(1) if W > 1 else logits.stride(0) if B > 1 else V
+    if (V > 1 and logits.stride(2) != 1) or row < V or (B > 1 and logits.stride(0) != W * row):
+        raise ValueError("the rows of logits must be contiguous and evenly spaced (strides %s)" % (logits.stride(),))
+    _need("scores", scores, torch.float32, (B, W), dev)
+    if finished is not None:
+        if eos is None:
+            raise ValueError("finished needs eos")
+        _need("finished", finished, torch.bool, (B, W), dev)
+    if eos is not None and not 0 <= eos < V:
+        raise ValueError("eos must be a token of the vocabulary of %d, got %s" % (V, eos))
+    n = W if n is None else int(n)
+    if not 1 <= n <= 64:
+        raise ValueError("n must be in [1, 64], got %d" % n)
+    out_scores = torch.empty(B, n, dtype=torch.float32, device=dev)
+    ids = torch.empty(2, B, n, dtype=torch.int32, device=dev)
+    out_finished = None if eos is None else torch.empty(B, n, dtype=torch.bool, device=dev)
+    n_ws = lib().kda_beam_select_workspace_bytes(B, W, V, n)
+    ws = torch.empty(n_ws, dtype=torch.uint8, device=dev)
+    _check(lib().kda_beam_select(context(dev).handle, B, W, V, n, _ptr(logits), dtype, row, _ptr(scores),
+                                 _ptr(finished), -1 if eos is None else int(eos), _ptr(out_scores), _ptr(ids[0]),
+                                 _ptr(ids[1]), _ptr(out_finished), _ptr(ws), n_ws, _stream(dev)), "kda_beam_select")
+    return out_scores, ids[0], ids[1], out_finished

@@ -13,7 +13,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libkda.so")
 SOURCES = [os.path.join(HERE, "csrc", f) for f in ("kda_kernels.hip", "kda_decode.hip", "gated_delta.hip",
-                                                  "kda_runtime.cpp", "gated_delta.cpp")]
+                                                  "state_pool.hip", "beam_select.hip", "kda_runtime.cpp",
+                                                  "gated_delta.cpp", "state_pool.cpp")]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

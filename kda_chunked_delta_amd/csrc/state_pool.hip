@@ -1,0 +1,296 @@
+// Pages of a state pool on gfx950: copying, forking, freeing and compacting
+// pages, and the reordering of a beam batch's states. A page is one slot of a
+// pool (H states of 64 KiB; with several layers, one page per layer), so all
+// of it is bound by HBM: two bytes moved per byte of a copied page.
+#include "state_pool_launch.h"
+
+namespace kda {
+namespace {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+// Bytes copied by one workgroup at a time: 256 threads, 4 vectors each in
+// flight.
+constexpr int MOVE_VEC = 4;
+constexpr int MOVE_PART = 256 * 16 * MOVE_VEC;
+
+// Part `part` of one page to another, by 256 threads.
+__device__ __forceinline__ void move_part(const PoolView& p, int layer, int src, int dst, int part) {
+    const uint8_t* s = p.base + layer * p.layer_stride + src * p.page_bytes;
+    uint8_t* d = p.base + layer * p.layer_stride + dst * p.page_bytes;
+    const int64_t at = (int64_t)part * MOVE_PART + threadIdx.x * 16;
+    u32x4 x[MOVE_VEC];
+#pragma unroll
+    for (int i = 0; i < MOVE_VEC; ++i)
+        if (at + i * 4096 < p.page_bytes) x[i] = __builtin_nontemporal_load((const u32x4*)(s + at + i * 4096));
+#pragma unroll
+    for (int i = 0; i < MOVE_VEC; ++i)
+        if (at + i * 4096 < p.page_bytes) __builtin_nontemporal_store(x[i], (u32x4*)(d + at + i * 4096));
+}
+
+__device__ __forceinline__ bool in_pool(const PoolView& p, int page) { return page >= 0 && page < p.n_pages; }
+
+__global__ __launch_bounds__(256) void pool_move(PoolView p, const int32_t* src, const int32_t* dst, int32_t n,
+                                                 int32_t parts) {
+    const int64_t per = (int64_t)parts * p.n_layers, total = per * n;
+    for (int64_t f = blockIdx.x; f < total; f += gridDim.x) {
+        const int i = (int)(f / per), rest = (int)(f % per);
+        const int a = src ? src[i] : i, b = dst[i];
+        if (a == b || !in_pool(p, a) || !in_pool(p, b)) continue;
+        move_part(p, rest / parts, a, b, rest % parts);
+    }
+}
+
+// Copies as if every source were read before any destination is written: each
+// workgroup holds its part (`vecs` vectors) of every source page in registers,
+// 8 vectors per thread, before it writes. Of several pairs with one
+// destination the last wins.
+__global__ __launch_bounds__(1024) void pool_copy(PoolView p, const int32_t* src, const int32_t* dst, int32_t n,
+                                                  int32_t parts, int32_t vecs) {
+    __shared__ int32_t to[kPoolCopyMax], from[kPoolCopyMax];
+    const int tid = threadIdx.x;
+    int d = -1;
+    if (tid < n) {
+        const int a = src[tid], b = dst[tid];
+        if (in_pool(p, a) && in_pool(p, b)) d = b;
+        from[tid] = a;
+        to[tid] = d;
+    }
+    __syncthreads();
+    if (d >= 0)
+        for (int j = tid + 1; j < n; ++j)
+            if (to[j] == d) d = -2;
+    __syncthreads();
+    if (tid < n) to[tid] = d;
+    __syncthreads();
+    const int layer = blockIdx.x / parts, part = blockIdx.x % parts;
+    uint8_t* base = p.base + layer * p.layer_stride;
+    u32x4 x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int f = tid + j * 1024, i = f / vecs;
+        const int64_t at = ((int64_t)part * vecs + f % vecs) * 16;
+        if (i < n && to[i] >= 0 && at < p.page_bytes) x[j] = *(const u32x4*)(base + from[i] * p.page_bytes + at);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int f = tid + j * 1024, i = f / vecs;
+        const int64_t at = ((int64_t)part * vecs + f % vecs) * 16;
+        if (i < n && to[i] >= 0 && at < p.page_bytes) *(u32x4*)(base + to[i] * p.page_bytes + at) = x[j];
+    }
+}
+
+// Exclusive prefix sum of x over 1024 threads; `all` gets the total. s_sum:
+// 17 ints of LDS, free again after the call.
+__device__ __forceinline__ int block_scan(int x, int* s_sum, int& all) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    int y = x;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int z = __shfl_up(y, d, 64);
+        if (lane >= d) y += z;
+    }
+    if (lane == 63) s_sum[wave] = y;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        int t = 0;
+        for (int w = 0; w < 16; ++w) {
+            const int c = s_sum[w];
+            s_sum[w] = t;
+            t += c;
+        }
+        s_sum[16] = t;
+    }
+    __syncthreads();
+    all = s_sum[16];
+    const int r = s_sum[wave] + y - x;
+    __syncthreads();
+    return r;
+}
+
+// Request i gets the free page of its rank among the requests with a used
+// source, in page order. One workgroup.
+__global__ __launch_bounds__(1024) void pool_fork_plan(uint8_t* used, int32_t n_pages, const int32_t* src,
+                                                       int32_t* dst, int32_t n) {
+    __shared__ int32_t s_sum[17], s_free[kPoolForkMax];
+    const int tid = threadIdx.x;
+    int want = 0;
+    int rank[kPoolForkMax / 1024];
+#pragma unroll
+    for (int j = 0; j < kPoolForkMax / 1024; ++j) {
+        rank[j] = -1;
+        if (j * 1024 < n) {
+            const int i = j * 1024 + tid, a = i < n ? src[i] : -1;
+            const bool ok = a >= 0 && a < n_pages && used[a];
+            int all;
+            const int r = block_scan(ok, s_sum, all);
+            if (ok) rank[j] = want + r;
+            want += all;
+        }
+    }
+    int found = 0;
+    for (int p0 = 0; p0 < n_pages && found < want; p0 += 1024) {
+        const int pg = p0 + tid;
+        const bool fr = pg < n_pages && !used[pg];
+        int all;
+        const int r = found + block_scan(fr, s_sum, all);
+        if (fr && r < want) s_free[r] = pg;
+        found += all;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kPoolForkMax / 1024; ++j) {
+        const int i = j * 1024 + tid;
+        if (i < n) {
+            const int d = rank[j] >= 0 && rank[j] < found ? s_free[rank[j]] : -1;
+            dst[i] = d;
+            if (d >= 0) used[d] = 1;
+        }
+    }
+}
+
+__global__ __launch_bounds__(256) void pool_free(uint8_t* used, int32_t n_pages, const int32_t* pages, int32_t n) {
+    const int i = blockIdx.x * 256 + threadIdx.x;
+    if (i >= n) return;
+    const int pg = pages[i];
+    if (pg >= 0 && pg < n_pages) used[pg] = 0;
+}
+
+// newpos[p] = the place of used page p among the first `live` pages: itself if
+// it lies there, else the hole of its rank; -1 for a free page. One workgroup.
+// The list of holes is kept in newpos behind the first `live` entries; the
+// final entries replace it from the last page down, because page p's rank
+// among the pages to move is at most p - live.
+__global__ __launch_bounds__(1024) void pool_compact_plan(uint8_t* used, int32_t n_pages, int32_t* table,
+                                                          int32_t n_table, int32_t* newpos, int32_t* n_live) {
+    __shared__ int32_t s_sum[17];
+    const int tid = threadIdx.x;
+    int live = 0;
+    for (int p0 = 0; p0 < n_pages; p0 += 1024) {
+        int all;
+        block_scan(p0 + tid < n_pages && used[p0 + tid], s_sum, all);
+        live += all;
+    }
+    int holes = 0;
+    for (int p0 = 0; p0 < live; p0 += 1024) {
+        const int pg = p0 + tid;
+        const bool hole = pg < live && !used[pg];
+        int all;
+        const int r = holes + block_scan(hole, s_sum, all);
+        if (hole) newpos[live + r] = pg;
+        if (pg < live) newpos[pg] = hole ? -1 : pg;
+        holes += all;
+    }
+    __syncthreads();
+    int behind = holes;  // pages to move at or after the current tile's end
+    for (int p0 = (n_pages - 1) / 1024 * 1024; p0 + 1024 > live && p0 >= 0; p0 -= 1024) {
+        const int pg = p0 + tid;
+        const bool mv = pg < n_pages && pg >= live && used[pg];
+        int all;
+        const int r = block_scan(mv, s_sum, all);
+        behind -= all;
+        const int to = mv ? newpos[live + behind + r] : -1;
+        __syncthreads();
+        if (pg < n_pages && pg >= live) newpos[pg] = to;
+    }
+    __syncthreads();
+    for (int pg = tid; pg < n_pages; pg += 1024) used[pg] = pg < live;
+    for (int i = tid; i < n_table; i += 1024) {
+        const int t = table[i];
+        table[i] = t >= 0 && t < n_pages ? newpos[t] : -1;
+    }
+    if (tid == 0) *n_live = live;
+}
+
+// Reordering of a beam batch. The first beam that continues parent q keeps q's
+// page; every other beam takes, in beam order, a page of the parents that no
+// beam continues (beams without a valid parent last, and uncopied). Sources
+// (pages of parents that go on) and destinations (pages of parents that do
+// not) are disjoint. One workgroup per part of one beam's page; each works the
+// plan of its batch entry out for itself, one beam per lane.
+__global__ __launch_bounds__(256) void beam_reorder(PoolView p, const int32_t* slots, const int32_t* parents,
+                                                    int32_t* new_slots, int32_t beams, int32_t parts) {
+    __shared__ int32_t s_target;
+    const int item = blockIdx.x / parts, part = blockIdx.x % parts;
+    const int w = item % beams;
+    const int64_t row = (int64_t)(item / beams) * beams;
+    if (threadIdx.x < 64) {
+        const int l = threadIdx.x;
+        int q = l < beams ? parents[row + l] : -1;
+        if (q >= beams) q = -1;
+        bool first = q >= 0, gone = l < beams;
+        for (int i = 0; i < beams; ++i) {
+            const int qi = __shfl(q, i, 64);
+            if (qi == q && i < l) first = false;
+            if (qi == l) gone = false;
+        }
+        const uint64_t extra = __ballot(q >= 0 && !first), none = __ballot(l < beams && q < 0);
+        uint64_t free = __ballot(gone);
+        const uint64_t below = (1ull << w) - 1;
+        int target = __shfl(q, w, 64);
+        const bool is_extra = extra >> w & 1, is_none = none >> w & 1;
+        if (is_extra || is_none) {
+            int r = is_extra ? __popcll(extra & below) : __popcll(extra) + __popcll(none & below);
+            for (; r > 0; --r) free &= free - 1;
+            target = __ffsll((unsigned long long)free) - 1;
+        }
+        if (l == 0) s_target = target;
+    }
+    __syncthreads();
+    const int to = slots[row + s_target], q = parents[row + w];
+    if (part == 0 && threadIdx.x == 0) new_slots[row + w] = to;
+    if (q < 0 || q >= beams) return;
+    const int from = slots[row + q];
+    if (from == to || !in_pool(p, from) || !in_pool(p, to)) return;
+    for (int layer = 0; layer < p.n_layers; ++layer) move_part(p, layer, from, to, part);
+}
+
+int parts_of(const PoolView& p) { return (int)((p.page_bytes + MOVE_PART - 1) / MOVE_PART); }
+
+}  // namespace
+
+hipError_t launch_pool_move(const PoolView& p, const int32_t* src, const int32_t* dst, int32_t n, hipStream_t s) {
+    const int parts = parts_of(p);
+    const int64_t total = (int64_t)parts * p.n_layers * n;
+    if (total == 0) return hipSuccess;
+    hipLaunchKernelGGL(pool_move, dim3((unsigned)(total < 4096 ? total : 4096)), dim3(256), 0, s, p, src, dst, n,
+                       parts);
+    return hipGetLastError();
+}
+
+hipError_t launch_pool_copy(const PoolView& p, const int32_t* src, const int32_t* dst, int32_t n, hipStream_t s) {
+    int vecs = 256;  // vectors of a part: 4 KiB down to 128 bytes, n parts within 8 vectors of 1024 threads
+    while (vecs * n > 8 * 1024) vecs >>= 1;
+    const int64_t parts = (p.page_bytes / 16 + vecs - 1) / vecs;
+    hipLaunchKernelGGL(pool_copy, dim3((unsigned)(parts * p.n_layers)), dim3(1024), 0, s, p, src, dst, n, (int)parts,
+                       vecs);
+    return hipGetLastError();
+}
+
+hipError_t launch_pool_fork_plan(uint8_t* used, int32_t n_pages, const int32_t* src, int32_t* dst, int32_t n,
+                                 hipStream_t s) {
+    hipLaunchKernelGGL(pool_fork_plan, dim3(1), dim3(1024), 0, s, used, n_pages, src, dst, n);
+    return hipGetLastError();
+}
+
+hipError_t launch_pool_free(uint8_t* used, int32_t n_pages, const int32_t* pages, int32_t n, hipStream_t s) {
+    hipLaunchKernelGGL(pool_free, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, used, n_pages, pages, n);
+    return hipGetLastError();
+}
+
+hipError_t launch_pool_compact_plan(uint8_t* used, int32_t n_pages, int32_t* table, int32_t n_table, int32_t* newpos,
+                                    int32_t* n_live, hipStream_t s) {
+    hipLaunchKernelGGL(pool_compact_plan, dim3(1), dim3(1024), 0, s, used, n_pages, table, n_table, newpos, n_live);
+    return hipGetLastError();
+}
+
+hipError_t launch_beam_reorder(const PoolView& p, const int32_t* slots, const int32_t* parents, int32_t* new_slots,
+                               int32_t batch, int32_t beams, hipStream_t s) {
+    const int parts = parts_of(p);
+    hipLaunchKernelGGL(beam_reorder, dim3((unsigned)((int64_t)batch * beams * parts)), dim3(256), 0, s, p, slots,
+                       parents, new_slots, beams, parts);
+    return hipGetLastError();
+}
+
+}  // namespace kda
