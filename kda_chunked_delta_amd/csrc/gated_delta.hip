@@ -19,6 +19,8 @@
 #include "gated_delta_launch.h"
 #include "kda_device.hpp"
 
+#include <mutex>
+
 namespace kda {
 namespace {
 
@@ -91,87 +93,88 @@ __device__ __forceinline__ HiLo split4(const f32x4& x) {
     return r;
 }
 
-// T' and A of a chunk as operands of 16x16x32 products: [row tile 2][hi, lo]
-// [lane 64][8 bf16], lane (gg, m) holding row m of the row tile and columns
-// 4gg + j (j < 4) and 16 + 4gg + j - 4 (j >= 4).
+// T' and A of a chunk as operands of 32x32x16 products: [step s 2][hi, lo]
+// [lane 64][8 bf16], lane l holding row l & 31 and columns 16s + 8 (j >> 2) +
+// 4 (l >> 5) + (j & 3). The wavefront that forms 16 x 16 tile (rt, ct) holds
+// row 16rt + m, columns 16ct + 4gg + v on lane (gg, m): half a lane's entry.
+// Tile (0, 1) is zero; it is cleared once and never written.
 constexpr int REC4 = 4096;
-__device__ __forceinline__ void put_half(uint8_t* rec, int rt, int half, int lane, const f32x4& x) {
+__device__ __forceinline__ void put_tile(uint8_t* rec, int rt, int ct, int lane, const f32x4& x) {
+    const int gg = lane >> 4, m = lane & 15;
+    uint8_t* at = rec + ct * 2048 + (32 * (gg & 1) + 16 * rt + m) * 16 + 8 * (gg >> 1);
     const HiLo s = split4(x);
-    *(u32x2*)(rec + ((rt * 2 + 0) * 64 + lane) * 16 + 8 * half) = s.h;
-    *(u32x2*)(rec + ((rt * 2 + 1) * 64 + lane) * 16 + 8 * half) = s.l;
+    *(u32x2*)at = s.h;
+    *(u32x2*)(at + 1024) = s.l;
 }
 
 __device__ __forceinline__ float pair_decay(float hr, float lr, float hi, float li) {
     return exp2_hw((hr - hi) + (lr - li));
 }
 
-// Scratch of the inverse, fp32: two 16 x 16 matrices per diagonal tile with a
-// row stride of 20 floats, T00 as lane (gg, m) -> T00[4gg + s][m], T11 as
-// lane (gg, m) -> T11[m][4gg + s].
+// Scratch of the inverse: 16 x 16 fp32 matrices with a row stride of 20 floats.
 constexpr int LSTR = 20;
 constexpr int LMAT = 16 * LSTR;
 
-// (I + L)^-1 of a diagonal 16 x 16 tile on one wavefront, both as t[s] =
-// T[4gg + s][m] (by rows) and u[s] = T[m][4gg + s] (by columns): 15 dependent
-// steps of a DPP broadcast and a multiply-subtract each.
-template <bool ROWS>
-__device__ __forceinline__ void invert_tile(const float* lt, int lane, f32x4& t, f32x4& u) {
-    const int gg = lane >> 4, m = lane & 15;
-    float lr[16], lc[16];  // L[m][K], L[K][m]
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const f32x4 a = *(const f32x4*)(lt + m * LSTR + 4 * q);
-#pragma unroll
-        for (int v = 0; v < 4; ++v) lr[4 * q + v] = a[v];
-        if constexpr (ROWS) {
-            const f32x4 b = *(const f32x4*)(lt + LMAT + m * LSTR + 4 * q);
-#pragma unroll
-            for (int v = 0; v < 4; ++v) lc[4 * q + v] = b[v];
-        }
-    }
-#pragma unroll
-    for (int s = 0; s < 4; ++s) t[s] = u[s] = (4 * gg + s == m) ? 1.f : 0.f;
-    auto step = [&](auto kc) __attribute__((always_inline)) {
-        constexpr int K = decltype(kc)::value;
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            u[s] -= lr[K] * row_newbcast<K>(u[s]);
-            if constexpr (ROWS) t[s] -= lc[15 - K] * row_newbcast<15 - K>(t[s]);
-        }
-    };
-    step(std::integral_constant<int, 0>{});  step(std::integral_constant<int, 1>{});
-    step(std::integral_constant<int, 2>{});  step(std::integral_constant<int, 3>{});
-    step(std::integral_constant<int, 4>{});  step(std::integral_constant<int, 5>{});
-    step(std::integral_constant<int, 6>{});  step(std::integral_constant<int, 7>{});
-    step(std::integral_constant<int, 8>{});  step(std::integral_constant<int, 9>{});
-    step(std::integral_constant<int, 10>{}); step(std::integral_constant<int, 11>{});
-    step(std::integral_constant<int, 12>{}); step(std::integral_constant<int, 13>{});
-    step(std::integral_constant<int, 14>{});
-}
-
-// Diagonal tile td of T': its rows go to the record, the unscaled inverse to
-// the scratch of the off-diagonal tile (T00 by rows, T11 by columns).
+// Diagonal tile td of T' on one wavefront. (I + L)^-1 is found by columns:
+// lane (gg, m) holds u[s] = T[m][4gg + s], and step K subtracts L[m][K] T[K][c]
+// from the rows below (a DPP broadcast of lane K inside a multiply-add, 15
+// dependent steps of 4). The unscaled tile stays behind for the off-diagonal
+// one, T00 as rows of LSTR floats in lt, T11 by lane in t11.
 template <int TD>
 __device__ __forceinline__ void diag_tile(const uint8_t* K, const float* gs, float* lt, float* inv, uint8_t* rec_t,
                                           int lane) {
     const int gg = lane >> 4, m = lane & 15, r0 = 16 * TD;
-    const f32x4 a = gram(K, r0, K, r0, lane);  // k_{4gg + v} . k_m
+    const f32x4 a = gram(K, r0, K, r0, lane);  // k_m . k_{4gg + v}
     const f32x4 hv = *(const f32x4*)(gs + GS_H + r0 + 4 * gg), lv = *(const f32x4*)(gs + GS_L + r0 + 4 * gg);
     const f32x4 bv = *(const f32x4*)(gs + GS_BETA + r0 + 4 * gg);
     const float hm = gs[GS_H + r0 + m], lm = gs[GS_L + r0 + m], bm = gs[GS_BETA + r0 + m];
-    f32x4 row, col;  // L[m][4gg + v], L[4gg + v][m]
+    f32x4 row;  // -L[m][4gg + v]
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-        row[v] = 4 * gg + v < m ? bm * a[v] * pair_decay(hm, lm, hv[v], lv[v]) : 0.f;
-        col[v] = m < 4 * gg + v ? bv[v] * a[v] * pair_decay(hv[v], lv[v], hm, lm) : 0.f;
-    }
+    for (int v = 0; v < 4; ++v) row[v] = 4 * gg + v < m ? -bm * a[v] * pair_decay(hm, lm, hv[v], lv[v]) : 0.f;
     *(f32x4*)(lt + m * LSTR + 4 * gg) = row;
-    if constexpr (TD == 0) *(f32x4*)(lt + LMAT + m * LSTR + 4 * gg) = col;
-    f32x4 t, u;
-    invert_tile<TD == 0>(lt, lane, t, u);
-    *(f32x4*)(inv + lane * 4) = TD == 0 ? t : u;
-    put_half(rec_t, TD, TD, lane, u * bv);
-    if constexpr (TD == 0) put_half(rec_t, 0, 1, lane, f32x4{0.f, 0.f, 0.f, 0.f});
+    float l[16];  // -L[m][K]
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const f32x4 x = *(const f32x4*)(lt + m * LSTR + 4 * q);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) l[4 * q + v] = x[v];
+    }
+    f32x4 u;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) u[s] = (4 * gg + s == m) ? 1.f : 0.f;
+    // A DPP read needs two wait states after the write of its source: three
+    // other instructions stand between them in the block, a nop before it.
+#define GD_STEP(K, L)                                                      \
+    "v_fmac_f32_dpp %0, %0, " L " row_newbcast:" K " row_mask:0xf bank_mask:0xf\n\t" \
+    "v_fmac_f32_dpp %1, %1, " L " row_newbcast:" K " row_mask:0xf bank_mask:0xf\n\t" \
+    "v_fmac_f32_dpp %2, %2, " L " row_newbcast:" K " row_mask:0xf bank_mask:0xf\n\t" \
+    "v_fmac_f32_dpp %3, %3, " L " row_newbcast:" K " row_mask:0xf bank_mask:0xf\n\t"
+    float u0 = u[0], u1 = u[1], u2 = u[2], u3 = u[3];
+    asm("s_nop 1\n\t"
+        GD_STEP("0", "%4")
+        GD_STEP("1", "%5")
+        GD_STEP("2", "%6")
+        GD_STEP("3", "%7")
+        GD_STEP("4", "%8")
+        GD_STEP("5", "%9")
+        GD_STEP("6", "%10")
+        GD_STEP("7", "%11")
+        GD_STEP("8", "%12")
+        GD_STEP("9", "%13")
+        GD_STEP("10", "%14")
+        GD_STEP("11", "%15")
+        GD_STEP("12", "%16")
+        GD_STEP("13", "%17")
+        GD_STEP("14", "%18")
+        "s_nop 1"
+        : "+v"(u0), "+v"(u1), "+v"(u2), "+v"(u3)
+        : "v"(l[0]), "v"(l[1]), "v"(l[2]), "v"(l[3]), "v"(l[4]), "v"(l[5]), "v"(l[6]), "v"(l[7]), "v"(l[8]), "v"(l[9]),
+          "v"(l[10]), "v"(l[11]), "v"(l[12]), "v"(l[13]), "v"(l[14]));
+#undef GD_STEP
+    u = f32x4{u0, u1, u2, u3};
+    if constexpr (TD == 0) *(f32x4*)(inv + m * LSTR + 4 * gg) = u;
+    else *(f32x4*)(inv + lane * 4) = u;
+    put_tile(rec_t, TD, TD, lane, u * bv);
 }
 
 // L10 as lane (gg, m) -> L10[4gg + v][m].
@@ -193,178 +196,438 @@ __device__ __forceinline__ f32x4 lower_tile(const uint8_t* K, const float* gs, i
 // T10[m][4gg + v], the record's layout.
 __device__ __forceinline__ void off_diagonal(const f32x4& l10, const float* t00, const float* t11, const float* gs,
                                              uint8_t* rec_t, int lane) {
-    const f32x4 a = *(const f32x4*)(t00 + lane * 4), b = *(const f32x4*)(t11 + lane * 4);
-    f32x4 y = {0.f, 0.f, 0.f, 0.f}, z = {0.f, 0.f, 0.f, 0.f};
+    const int gg = lane >> 4, m = lane & 15;
+    const f32x4 b = *(const f32x4*)(t11 + lane * 4);
+    f32x4 a, y = {0.f, 0.f, 0.f, 0.f}, z = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < 4; ++s) a[s] = t00[(4 * gg + s) * LSTR + m];
 #pragma unroll
     for (int s = 0; s < 4; ++s) y = mfma_f32_k4(l10[s], b[s], y);
 #pragma unroll
     for (int s = 0; s < 4; ++s) z = mfma_f32_k4(a[s], y[s], z);
-    const f32x4 bv = *(const f32x4*)(gs + GS_BETA + 4 * (lane >> 4));
-    put_half(rec_t, 1, 0, lane, -z * bv);
+    const f32x4 bv = *(const f32x4*)(gs + GS_BETA + 4 * gg);
+    put_tile(rec_t, 1, 0, lane, -z * bv);
 }
 
-// A (masked, decayed q-k products) to its record.
-__device__ __forceinline__ void qk_tiles(const uint8_t* Q, const uint8_t* K, const float* gs, uint8_t* rec_a, int lane) {
+// A (masked, decayed q-k products, times the output's scale) to its record.
+__device__ __forceinline__ void qk_tiles(const uint8_t* Q, const uint8_t* K, const float* gs, float scale,
+                                         uint8_t* rec_a, int lane) {
     const int gg = lane >> 4, m = lane & 15;
 #pragma unroll
     for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
-        for (int ct = 0; ct < 2; ++ct) {
-            f32x4 r = {0.f, 0.f, 0.f, 0.f};
-            if (ct <= rt) {
-                const f32x4 a = gram(K, 16 * ct, Q, 16 * rt, lane);  // k_{4gg + v} . q_m
-                const f32x4 hv = *(const f32x4*)(gs + GS_H + 16 * ct + 4 * gg);
-                const f32x4 lv = *(const f32x4*)(gs + GS_L + 16 * ct + 4 * gg);
-                const float hm = gs[GS_H + 16 * rt + m], lm = gs[GS_L + 16 * rt + m];
+        for (int ct = 0; ct <= rt; ++ct) {
+            const f32x4 a = gram(K, 16 * ct, Q, 16 * rt, lane);  // k_{4gg + v} . q_m
+            const f32x4 hv = *(const f32x4*)(gs + GS_H + 16 * ct + 4 * gg);
+            const f32x4 lv = *(const f32x4*)(gs + GS_L + 16 * ct + 4 * gg);
+            const float hm = gs[GS_H + 16 * rt + m], lm = gs[GS_L + 16 * rt + m];
+            f32x4 r;
 #pragma unroll
-                for (int v = 0; v < 4; ++v)
-                    r[v] = (ct < rt || 4 * gg + v <= m) ? a[v] * pair_decay(hm, lm, hv[v], lv[v]) : 0.f;
-            }
-            put_half(rec_a, rt, ct, lane, r);
+            for (int v = 0; v < 4; ++v)
+                r[v] = (ct < rt || 4 * gg + v <= m) ? scale * a[v] * pair_decay(hm, lm, hv[v], lv[v]) : 0.f;
+            put_tile(rec_a, rt, ct, lane, r);
         }
 }
 
-// The state of one wavefront: NT tiles of 16 value columns. S[2p + e][n] holds,
-// on lane (gg, m), channels 32p + 8gg + 4e + v of column 16n + m: two tiles
-// together are one 16x16x32 operand with 8 consecutive channels per lane.
-template <int NT>
-struct State {
-    f32x4 s[8][NT];
+// 32 x 32 products. A and B operands: lane l holds row (column) l & 31 and 8
+// of the 16 summed indices, those of its half h = l >> 5. Result: lane l holds
+// column l & 31 and rows 8a + 4h + b in element 4a + b.
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+__device__ __forceinline__ f32x16 mfma_32(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0,
+                                                   0, 0);
+}
+__device__ __forceinline__ f32x4 quarter(const f32x16& x, int a) {
+    return f32x4{x[4 * a], x[4 * a + 1], x[4 * a + 2], x[4 * a + 3]};
+}
+// Elements 8s .. 8s + 7 of a result as the operand of step s of a product that
+// sums over its rows: the lane's 8 indices are rows 16s + 8 (j >> 2) + 4h + (j & 3).
+struct Operand {
+    u32x4 h[2], l[2];
+};
+__device__ __forceinline__ void pack_rows(const f32x16& x, u32x4 (&y)[2]) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        const u32x2 a = pack4(quarter(x, 2 * s)), b = pack4(quarter(x, 2 * s + 1));
+        y[s] = u32x4{a.x, a.y, b.x, b.y};
+    }
+}
+// The rest x - hi of a tile is formed by the matrix unit, as x + (-1) hi with
+// the operand of -1 in minus_one[s]. It is exact, and two matrix instructions
+// stand in for 32 vector ones, which bound the chain otherwise.
+struct MinusOne {
+    u32x4 s[2];
+};
+__device__ __forceinline__ MinusOne minus_one(int lane) {
+    const int row = lane & 31, h = lane >> 5;
+    MinusOne m;
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const int r = row - (16 * s + 8 * (w >> 1) + 4 * h + 2 * (w & 1));  // 0: the low half, 1: the high
+            m.s[s][w] = r == 0 ? 0x0000bf80u : r == 1 ? 0xbf800000u : 0u;
+        }
+    return m;
+}
+__device__ __forceinline__ f32x16 rest_of(const f32x16& x, const u32x4 (&hi)[2], const MinusOne& m) {
+    return mfma_32(m.s[1], hi[1], mfma_32(m.s[0], hi[0], x));
+}
+
+// The state of one wavefront: 32 value columns in four tiles of 32 channels.
+// Row 8a + 4h + b of tile t is channel 32t + 16 (a >> 1) + 8h + 4 (a & 1) + b,
+// so that step s of tile t takes 8 consecutive channels 32t + 16s + 8h ..
+// from each lane of the other operand. Column n of the tiles is value column
+// value_col(n), so that a lane's 16 rows of a transposed result are 16
+// consecutive value columns.
+__device__ __forceinline__ int value_col(int n) { return 16 * ((n >> 2) & 1) + 4 * (n >> 3) + (n & 3); }
+
+// A lane's place in an LDS tile, from which the places of the other steps
+// follow by an exclusive or. (Kept from the optimiser, which would hold every
+// place in a register of its own.)
+__device__ __forceinline__ int opaque(int x) {
+    asm("" : "+v"(x));
+    return x;
+}
+
+// Scheduling: nothing moves across sched_fence, and interleave<M, V>(n) asks
+// for n groups of M matrix and V vector instructions.
+__device__ __forceinline__ void sched_fence() { __builtin_amdgcn_sched_barrier(0); }
+// Fixes the place of what forms or uses x among the other pins.
+template <class T>
+__device__ __forceinline__ void pin(T& x) { asm volatile("" : "+v"(x)); }
+template <int N, int M, int V>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x8, M, 0);
+        __builtin_amdgcn_sched_group_barrier(0x2, V, 0);
+    }
+}
+// What is left of a chunk's output when its state is done: o (scaled by gam)
+// and the operands of A U.
+struct Rest {
+    f32x16 o;
+    Operand u, a;
 };
 
-// Advances the state over one chunk; with OUT, o[rt][n] gets the unscaled
-// output of token 16rt + m, columns 16n + 4gg + v.
-template <int NT, bool OUT>
+// o += A U: token l & 31, element 4a + b being value column 16h + 4a + b.
+__device__ __forceinline__ void finish_output(Rest& x) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) x.o = mfma_32(x.u.l[s], x.a.h[s], x.o);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) x.o = mfma_32(x.u.h[s], x.a.l[s], x.o);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) x.o = mfma_32(x.u.h[s], x.a.h[s], x.o);
+}
+
+__device__ __forceinline__ Operand load_record(const uint8_t* rec, int lane) {
+    Operand r;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        r.h[s] = *(const u32x4*)(rec + s * 2048 + lane * 16);
+        r.l[s] = *(const u32x4*)(rec + s * 2048 + 1024 + lane * 16);
+    }
+    return r;
+}
+
+// Advances the state over one chunk and, with OUT, finishes and stores the
+// output of the one before it. The matrix unit is to be busy throughout (76
+// instructions of 32 cycles with OUT): the last chunk's A U and K S go beside
+// the split and the scaling of S, Q S beside R = V - diag(gam) K S and beside
+// W, K^T W beside the split of U. LDS operands are read a phase ahead.
+template <bool OUT, class Store>
 __device__ __forceinline__ void chunk_step(const uint8_t* Q, const uint8_t* K, const uint8_t* V, const uint8_t* rec_t,
-                                           const uint8_t* rec_a, const float* gs, int col0, int lane, State<NT>& st,
-                                           f32x4 (&o)[2][NT]) {
-    const int gg = lane >> 4, m = lane & 15, tr = (lane >> 2) & 3, tc = lane & 3;
-    const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-    f32x4 P[2][NT];
-#pragma unroll
-    for (int rt = 0; rt < 2; ++rt)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) P[rt][n] = o[rt][n] = zero;
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-        u32x4 sh[NT], sl[NT];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const HiLo a = split4(st.s[2 * p][n]), b = split4(st.s[2 * p + 1][n]);
-            sh[n] = u32x4{a.h.x, a.h.y, b.h.x, b.h.y};
-            sl[n] = u32x4{a.l.x, a.l.y, b.l.x, b.l.y};
-        }
-#pragma unroll
-        for (int rt = 0; rt < 2; ++rt) {
-            const u32x4 kf = row_frag(K, 16 * rt, p, lane);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                P[rt][n] = mfma_k32(kf, sh[n], P[rt][n]);
-                P[rt][n] = mfma_k32(kf, sl[n], P[rt][n]);
-            }
-            if constexpr (OUT) {
-                const u32x4 qf = row_frag(Q, 16 * rt, p, lane);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    o[rt][n] = mfma_k32(sh[n], qf, o[rt][n]);
-                    o[rt][n] = mfma_k32(sl[n], qf, o[rt][n]);
-                }
-            }
-        }
-    }
-    // R = V - diag(gam) P, then U = T' R
-    u32x4 rh[NT], rl[NT], uh[NT], ul[NT], wh[NT], wl[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        HiLo r[2];
-#pragma unroll
-        for (int rt = 0; rt < 2; ++rt) {
-            const f32x4 gam = *(const f32x4*)(gs + GS_GAM + 16 * rt + 4 * gg);
-            const u32x2 vw = lds_load_tr16(V + tile_off(16 * rt + 4 * gg + tr, (col0 >> 3) + 2 * n + (tc >> 1)) +
-                                           8 * (tc & 1));
-            r[rt] = split4(f32x4{bf16_lo(vw.x) - gam[0] * P[rt][n][0], bf16_hi(vw.x) - gam[1] * P[rt][n][1],
-                                 bf16_lo(vw.y) - gam[2] * P[rt][n][2], bf16_hi(vw.y) - gam[3] * P[rt][n][3]});
-        }
-        rh[n] = u32x4{r[0].h.x, r[0].h.y, r[1].h.x, r[1].h.y};
-        rl[n] = u32x4{r[0].l.x, r[0].l.y, r[1].l.x, r[1].l.y};
-    }
-    f32x4 U[2][NT];
-#pragma unroll
-    for (int rt = 0; rt < 2; ++rt) {
-        const u32x4 th = *(const u32x4*)(rec_t + ((rt * 2 + 0) * 64 + lane) * 16);
-        const u32x4 tl = *(const u32x4*)(rec_t + ((rt * 2 + 1) * 64 + lane) * 16);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            f32x4 u = mfma_k32(tl, rh[n], zero);
-            u = mfma_k32(th, rl[n], u);
-            U[rt][n] = mfma_k32(th, rh[n], u);
-        }
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        HiLo w[2], u[2];
-#pragma unroll
-        for (int rt = 0; rt < 2; ++rt) {
-            const f32x4 last = *(const f32x4*)(gs + GS_LAST + 16 * rt + 4 * gg);
-            w[rt] = split4(last * U[rt][n]);
-            if constexpr (OUT) u[rt] = split4(U[rt][n]);
-        }
-        wh[n] = u32x4{w[0].h.x, w[0].h.y, w[1].h.x, w[1].h.y};
-        wl[n] = u32x4{w[0].l.x, w[0].l.y, w[1].l.x, w[1].l.y};
-        if constexpr (OUT) {
-            uh[n] = u32x4{u[0].h.x, u[0].h.y, u[1].h.x, u[1].h.y};
-            ul[n] = u32x4{u[0].l.x, u[0].l.y, u[1].l.x, u[1].l.y};
-        }
-    }
-    // S = gam_31 S + K^T W
+                                           const uint8_t* rec_a, const float* gs, float scale, int col0, int lane,
+                                           const MinusOne& neg, f32x16 (&S)[4], Rest& rest, Store store) {
+    const int h = lane >> 5, odd = (lane >> 4) & 1, r = (lane >> 2) & 3, c = lane & 3;
+    const f32x16 zero = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    // rows l & 31, the granule of step s of tile t: 4t + 2s + h
+    const int at_row = opaque(tile_off(lane & 31, h));
+    auto row32 = [&](const uint8_t* tile, int t, int s) __attribute__((always_inline)) {
+        return *(const u32x4*)(tile + (at_row ^ ((4 * t + 2 * s) << 4)));
+    };
+    u32x4 kf[4][2];
     const float gc = gs[GS_GAM + 31];
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-        const int gi = 4 * (t >> 1) + tc, e = 8 * (t & 1);
-        const u32x2 k0 = lds_load_tr16(K + tile_off(4 * gg + tr, gi) + e);
-        const u32x2 k1 = lds_load_tr16(K + tile_off(16 + 4 * gg + tr, gi) + e);
-        const u32x4 kt = {k0.x, k0.y, k1.x, k1.y};
+    for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            f32x4 s = gc * st.s[t][n];
-            s = mfma_k32(kt, wl[n], s);
-            st.s[t][n] = mfma_k32(kt, wh[n], s);
+        for (int s = 0; s < 2; ++s) kf[t][s] = row32(K, t, s);
+    if constexpr (OUT) finish_output(rest);
+    sched_fence();
+    // K S
+    Operand sb[4];
+    f32x16 P = zero, below[2];
+    u32x4 qf[4][2];
+    f32x4 gam[4];
+    u32x2 vw[4];
+#pragma unroll
+    for (int t = 0; t <= 4; ++t) {
+        if (t < 4) {
+            pack_rows(S[t], sb[t].h);
+            below[t & 1] = rest_of(S[t], sb[t].h, neg);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) P = mfma_32(kf[t][s], sb[t].h[s], P);
         }
-    }
-    if constexpr (OUT) {
+        if constexpr (OUT)
+            if (t == 1) store(rest.o);
+        if (t == 3) {
 #pragma unroll
-        for (int rt = 0; rt < 2; ++rt) {
-            const float gam = gs[GS_GAM + 16 * rt + m];
-            const u32x4 ah = *(const u32x4*)(rec_a + ((rt * 2 + 0) * 64 + lane) * 16);
-            const u32x4 al = *(const u32x4*)(rec_a + ((rt * 2 + 1) * 64 + lane) * 16);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                f32x4 x = gam * o[rt][n];
-                x = mfma_k32(ul[n], ah, x);
-                x = mfma_k32(uh[n], al, x);
-                o[rt][n] = mfma_k32(uh[n], ah, x);
+            for (int a = 0; a < 4; ++a) {
+                gam[a] = *(const f32x4*)(gs + GS_GAM + 8 * a + 4 * h);
+                // rows 8a + 4h + r, the lane's column value_col(l & 31)
+                vw[a] = lds_load_tr16(V + tile_off(8 * a + 4 * h + r, (col0 >> 3) + 2 * (c & 1) + odd) + 8 * (c >> 1));
             }
         }
+        if constexpr (OUT)
+            if (t == 4) {
+#pragma unroll
+                for (int s = 0; s < 4; ++s) qf[s >> 1][s & 1] = row32(Q, s >> 1, s & 1);
+            }
+        if (t > 0) {
+            pack_rows(below[(t - 1) & 1], sb[t - 1].l);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) P = mfma_32(kf[t - 1][s], sb[t - 1].l[s], P);
+            S[t - 1] = gc * S[t - 1];
+        }
+        sched_fence();
     }
+    // R = V - diag(gam) K S
+    f32x16 o = zero;
+    int done = 0;
+    auto qs = [&](int n) __attribute__((always_inline)) {  // the next n of Q S
+        if constexpr (OUT) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k < n) {
+                    const int q = done + k, t = q >> 2, s = q & 1;
+                    pin(qf[t][s]);
+                    o = mfma_32(q & 2 ? sb[t].l[s] : sb[t].h[s], qf[t][s], o);
+                }
+            done += n;
+        }
+        sched_fence();
+    };
+    f32x16 R;
+    Operand T;
+    qs(2);
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+        f32x4 x = {__builtin_fmaf(-gam[a][0], P[4 * a], bf16_lo(vw[a].x)),
+                   __builtin_fmaf(-gam[a][1], P[4 * a + 1], bf16_hi(vw[a].x)),
+                   __builtin_fmaf(-gam[a][2], P[4 * a + 2], bf16_lo(vw[a].y)),
+                   __builtin_fmaf(-gam[a][3], P[4 * a + 3], bf16_hi(vw[a].y))};
+        pin(x);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) R[4 * a + b] = x[b];
+        if (a == 1) T = load_record(rec_t, lane);
+        qs(1);
+    }
+    Operand rb;
+    pack_rows(R, rb.h);
+    const f32x16 R_below = rest_of(R, rb.h, neg);
+    if constexpr (OUT) {
+#pragma unroll
+        for (int s = 4; s < 8; ++s) qf[s >> 1][s & 1] = row32(Q, s >> 1, s & 1);
+    }
+    sched_fence();
+    qs(2);
+    // U = T' R
+    f32x16 U = zero;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) U = mfma_32(T.l[s], rb.h[s], U);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) U = mfma_32(T.h[s], rb.h[s], U);
+    pack_rows(R_below, rb.l);
+    f32x4 last[4];
+#pragma unroll
+    for (int a = 0; a < 4; ++a) last[a] = *(const f32x4*)(gs + GS_LAST + 8 * a + 4 * h);
+    float gm = 0.f;
+    if constexpr (OUT) gm = scale * gs[GS_GAM + (lane & 31)];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) U = mfma_32(T.h[s], rb.l[s], U);
+    sched_fence();
+    // K^T: lane row l & 31 of tile t is channel 32t + 16 odd + 8 (i >> 2 & 1) + 4 (i >> 3) + (i & 3), i = l & 15
+    const int at_col0 = opaque(tile_off(4 * h + r, 2 * odd + (c & 1)) + 8 * (c >> 1));
+    const int at_col1 = opaque(tile_off(8 + 4 * h + r, 2 * odd + (c & 1)) + 8 * (c >> 1));
+    u32x4 kt[4][2];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const u32x2 k0 = lds_load_tr16(K + (at_col0 ^ (4 * t << 4)) + 4096 * s);
+            const u32x2 k1 = lds_load_tr16(K + (at_col1 ^ (4 * t << 4)) + 4096 * s);
+            kt[t][s] = u32x4{k0.x, k0.y, k1.x, k1.y};
+        }
+    sched_fence();
+    qs(3);
+    // W = diag(exp(G_31 - G)) U
+    f32x16 W;
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int b = 0; b < 4; ++b) W[4 * a + b] = last[a][b] * U[4 * a + b];
+    Operand wb;
+    pack_rows(W, wb.h);
+    const f32x16 W_below = rest_of(W, wb.h, neg);
+    if constexpr (OUT) rest.a = load_record(rec_a, lane);
+    sched_fence();
+    qs(5);
+    pack_rows(W_below, wb.l);
+    sched_fence();
+    // S += K^T W beside the split of U
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) S[t] = mfma_32(kt[t][s], wb.h[s], S[t]);
+    if constexpr (OUT) {
+        pack_rows(U, rest.u.h);
+        rest.o = gm * o;
+        const f32x16 U_below = rest_of(U, rest.u.h, neg);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) S[t] = mfma_32(kt[t][s], wb.l[s], S[t]);
+        pack_rows(U_below, rest.u.l);
+    } else {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) S[t] = mfma_32(kt[t][s], wb.l[s], S[t]);
+    }
+    sched_fence();
 }
 
 __device__ __forceinline__ float load_state(const void* p, int64_t i, bool bf16) {
     return bf16 ? __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16) : ((const float*)p)[i];
 }
 
-// The channel of row v of tile t on lane group gg.
-__device__ __forceinline__ int state_channel(int t, int gg, int v) { return 32 * (t >> 1) + 8 * gg + 4 * (t & 1) + v; }
+// Prefill: one workgroup of 8 wavefronts per (unit, head, column tile), in
+// a software pipeline with one barrier per chunk. In interval i
+//   wavefronts 4 .. 7 advance the state over chunk i (16 NT columns each);
+//   wavefronts 0 .. 3 form the operands of later chunks: 0, 1 and 2 the tiles
+//     of (I + L)^-1 of chunk i + 2 and 3 its A, wavefront 2 also T10 of chunk
+//     i + 1 (from the tiles published by the last barrier) and the row values
+//     of chunk i + 3, and all four issue the loads of q, k (chunk i + 4) and v
+//     (chunk i + 2), which must have landed by the end of interval i + 1.
+// Ring slots: q and k 5 chunks, v and the operands 3, the row values 4.
+constexpr int N_QK = 5, N_V = 3, N_REC = 3, N_GS = 4;
+constexpr int DEPTH = 4;  // intervals from a chunk's first load to its use
+template <bool OUT>
+struct Lds {
+    alignas(16) uint8_t k[N_QK][TILE_BYTES];
+    alignas(16) uint8_t q[OUT ? N_QK : 1][TILE_BYTES];
+    alignas(16) uint8_t v[N_V][TILE_BYTES];
+    alignas(16) uint8_t t[N_REC][REC4];
+    alignas(16) uint8_t a[OUT ? N_REC : 1][REC4];
+    alignas(16) float gs[N_GS][GS_FLOATS];
+    alignas(16) float lt[2 * LMAT];
+    alignas(16) float t00[2][LMAT], t11[2][256];
+};
 
-template <int NT, bool OUT>
+// Ring positions of chunks i .. i + N - 1 (uniform).
+template <int N>
+struct Ring {
+    int at[N];
+    __device__ __forceinline__ Ring() {
+#pragma unroll
+        for (int j = 0; j < N; ++j) at[j] = j;
+    }
+    __device__ __forceinline__ void next() {
+        const int first = at[0];
+#pragma unroll
+        for (int j = 0; j + 1 < N; ++j) at[j] = at[j + 1];
+        at[N - 1] = first;
+    }
+};
+
+// Valid rows of chunk c of a unit of n tokens (0 outside it).
+__device__ __forceinline__ int rows_of_chunk(int n, int c) {
+    const int left = n - c * GC;
+    return __builtin_amdgcn_readfirstlane(c < 0 || left <= 0 ? 0 : left < GC ? left : GC);
+}
+
+// What a workgroup works on (uniform).
+struct GdWork {
+    const uint8_t *q, *k, *v;  // the unit's first rows of its head
+    const float* g;            // beta at the same index
+    const void* beta;
+    uint32_t st_qk, st_v;      // bytes from row to row
+    int H, n_tok, n_chunks;
+    float scale;
+    bool beta_bf16, with_v;
+};
+
+// The loop of operand wavefront ROLE (a loop per role: values that one role
+// carries from interval to interval would make the others wait for its loads).
+template <int ROLE, bool OUT>
+__device__ __forceinline__ void produce(const GdWork& w, Lds<OUT>& lds, int lane) {
+    Ring<N_QK> qk;
+    Ring<N_V> rv;
+    Ring<N_REC> rec;
+    Ring<N_GS> gs;
+    // a chunk's rows by the four wavefronts, 8 each
+    auto load = [&](const uint8_t* base, uint32_t stride, int c, int rows, uint8_t* tile) __attribute__((always_inline)) {
+        const auto rsrc = chunk_rsrc(base + (size_t)(c < 0 ? 0 : c) * GC * stride, (uint32_t)rows * stride);
+        load_rows(rsrc, stride, 2 * ROLE, lane, tile);
+        load_rows(rsrc, stride, 2 * ROLE + 1, lane, tile);
+    };
+    float x = 0.f;  // ROLE 2: log-decay of row lane & 31, and its beta's bits
+    uint32_t b = 0;
+    f32x4 l10 = {0.f, 0.f, 0.f, 0.f};
+    // ring position j is chunk i + j
+    for (int i = -DEPTH; i < w.n_chunks; ++i) {
+        const int par = i & 1, rows = rows_of_chunk(w.n_tok, i + 4);
+        load(w.v, w.st_v, i + 2, w.with_v ? rows_of_chunk(w.n_tok, i + 2) : 0, lds.v[rv.at[2]]);
+        load(w.k, w.st_qk, i + 4, rows, lds.k[qk.at[4]]);
+        if constexpr (OUT) load(w.q, w.st_qk, i + 4, rows, lds.q[qk.at[4]]);
+        const bool inside = i + 2 >= 0 && i + 2 < w.n_chunks;
+        const float* g = lds.gs[gs.at[2]];
+        const uint8_t* K = lds.k[qk.at[2]];
+        if constexpr (ROLE == 0) {
+            if (inside) diag_tile<0>(K, g, lds.lt, lds.t00[par], lds.t[rec.at[2]], lane);
+        } else if constexpr (ROLE == 1) {
+            if (inside) diag_tile<1>(K, g, lds.lt + LMAT, lds.t11[par], lds.t[rec.at[2]], lane);
+        } else if constexpr (ROLE == 3) {
+            if constexpr (OUT)
+                if (inside) qk_tiles(lds.q[qk.at[2]], K, g, w.scale, lds.a[rec.at[2]], lane);
+        } else {
+            if (i + 1 >= 0 && i + 1 < w.n_chunks)
+                off_diagonal(l10, lds.t00[par ^ 1], lds.t11[par ^ 1], lds.gs[gs.at[1]], lds.t[rec.at[1]], lane);
+            if (inside) l10 = lower_tile(K, g, lane);
+            row_scan(x, w.beta_bf16 ? __uint_as_float(b << 16) : __uint_as_float(b), lane, lds.gs[gs.at[3]]);
+            const uint32_t at = (uint32_t)(lane & 31) * (uint32_t)w.H, n = rows ? (uint32_t)(rows - 1) * w.H + 1 : 0u;
+            const size_t c = (size_t)(i + 4) * GC * w.H;
+            x = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(chunk_rsrc(w.g + c, n * 4),
+                                                                               (int)(at * 4), 0, 0));
+            if (w.beta_bf16)
+                b = __builtin_amdgcn_raw_buffer_load_b16(chunk_rsrc((const uint16_t*)w.beta + c, n * 2), (int)(at * 2),
+                                                         0, 0);
+            else
+                b = __builtin_amdgcn_raw_buffer_load_b32(chunk_rsrc((const float*)w.beta + c, n * 4), (int)(at * 4), 0,
+                                                         0);
+        }
+        // the loads of the last interval have landed (role 2 has waited for its own, to scan them)
+        if constexpr (ROLE != 2) {
+            if constexpr (OUT) asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
+            else asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
+        }
+        lds_barrier();
+        qk.next();
+        rv.next();
+        rec.next();
+        gs.next();
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS outlives the workgroup
+}
+
+template <bool OUT>
 __global__ __launch_bounds__(512) void gd_prefill(GdArgs a) {
-    constexpr int COLS = 64 * NT, NCT = D / COLS;
-    __shared__ __align__(16) uint8_t sQ[TILE_BYTES], sK[TILE_BYTES], sV[TILE_BYTES], sT_[REC4], sA[REC4];
-    __shared__ __align__(16) float gs[GS_FLOATS], lt[3 * LMAT], t00[256], t11[256];
+    extern __shared__ __align__(16) uint8_t lds_raw[];
+    Lds<OUT>& lds = *(Lds<OUT>*)lds_raw;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int gg = lane >> 4, m = lane & 15;
-    const int ct = blockIdx.x % NCT, uh = blockIdx.x / NCT;
-    const int h = uh % a.H;
-    const GdUnit un = a.units[uh / a.H];
+    const int h = blockIdx.x % a.H;
+    const GdUnit un = a.units[blockIdx.x / a.H];
     // the unit's tokens, clamped into the sequence and the inputs
     int64_t beg = a.cu[un.seq], end = a.cu[un.seq + 1];
     end = end > a.Tt ? a.Tt : end;
@@ -372,93 +635,119 @@ __global__ __launch_bounds__(512) void gd_prefill(GdArgs a) {
     end = end < beg + un.n_tok ? end : beg + un.n_tok;
     const int n_tok = __builtin_amdgcn_readfirstlane(end > beg ? (int)(end - beg) : 0);
     const int n_chunks = (n_tok + GC - 1) / GC;
-    const uint32_t st_qk = (uint32_t)a.Hk * (D * 2), st_v = (uint32_t)a.H * (D * 2);
-    const uint8_t* qb = (const uint8_t*)a.q + (beg * a.Hk + h / a.group) * (D * 2);
-    const uint8_t* kb = (const uint8_t*)a.k + (beg * a.Hk + h / a.group) * (D * 2);
-    const uint8_t* vb = (const uint8_t*)a.v + (beg * a.H + h) * (D * 2);
-    uint8_t* ob = (uint8_t*)a.out + (beg * a.H + h) * (D * 2);
+    const uint32_t st_v = (uint32_t)a.H * (D * 2);
 
-    const bool chain = wave >= 4;  // wavefronts 4 .. 7 hold the state
-    const int col0 = ct * COLS + (wave - 4) * (16 * NT);
-    State<NT> st;
-    if (chain) {
-        const void* src = un.in >= 0 ? (const void*)(a.carries + ((int64_t)un.in * a.H + h) * (D * D))
-                                     : (const void*)a.s0;
-        const bool b16 = un.in < 0 && a.state_bf16;
-        const int64_t base = un.in >= 0 ? 0 : ((int64_t)un.seq * a.H + h) * (D * D);
-        const bool load = un.in >= 0 || (un.in == GD_INITIAL && a.s0);
-#pragma unroll
-        for (int t = 0; t < 8; ++t)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const int ch = state_channel(t, gg, v), col = col0 + 16 * n + m;
-                    st.s[t][n][v] = load ? load_state(src, base + ch * D + col, b16)
-                                         : (un.in == GD_IDENTITY && ch == col ? 1.f : 0.f);
-                }
+    if (wave < 4) {
+        GdWork w;
+        const int64_t row = beg * a.H + h, row_qk = (beg * a.Hk + h / a.group) * (D * 2);
+        w.q = (const uint8_t*)a.q + row_qk;
+        w.k = (const uint8_t*)a.k + row_qk;
+        w.v = (const uint8_t*)a.v + row * (D * 2);
+        w.g = a.g + row;
+        w.beta = a.beta_bf16 ? (const void*)((const uint16_t*)a.beta + row) : (const void*)((const float*)a.beta + row);
+        w.st_qk = (uint32_t)a.Hk * (D * 2);
+        w.st_v = st_v;
+        w.H = a.H;
+        w.n_tok = n_tok;
+        w.n_chunks = n_chunks;
+        w.scale = a.scale;
+        w.beta_bf16 = a.beta_bf16;
+        w.with_v = un.with_v;
+        if (wave == 0) produce<0, OUT>(w, lds, lane);
+        else if (wave == 1) produce<1, OUT>(w, lds, lane);
+        else if (wave == 2) produce<2, OUT>(w, lds, lane);
+        else produce<3, OUT>(w, lds, lane);
+        return;
     }
-    for (int ci = 0; ci < n_chunks; ++ci) {
-        const int left = n_tok - ci * GC, nrows = left < GC ? left : GC;
-        __syncthreads();  // the tiles of the last chunk are free
-        {
-            const size_t cq = (size_t)ci * GC * st_qk, cv = (size_t)ci * GC * st_v;
-            load_rows(chunk_rsrc(kb + cq, (uint32_t)nrows * st_qk), st_qk, wave, lane, sK);
-            load_rows(chunk_rsrc(vb + cv, un.with_v ? (uint32_t)nrows * st_v : 0u), st_v, wave, lane, sV);
-            if constexpr (OUT) load_rows(chunk_rsrc(qb + cq, (uint32_t)nrows * st_qk), st_qk, wave, lane, sQ);
-        }
-        if (wave == 0) {
-            const int r = lane & 31;
-            float x = 0.f, b = 0.f;
-            if (r < nrows) {
-                const int64_t i = (beg + ci * GC + r) * a.H + h;
-                x = a.g[i];
-                b = a.beta_bf16 ? __uint_as_float((uint32_t)((const uint16_t*)a.beta)[i] << 16)
-                                : ((const float*)a.beta)[i];
-            }
-            row_scan(x, b, lane, gs);
-        }
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        f32x4 l10 = {0.f, 0.f, 0.f, 0.f};
-        if (wave == 0) diag_tile<0>(sK, gs, lt, t00, sT_, lane);
-        else if (wave == 1) diag_tile<1>(sK, gs, lt + 2 * LMAT, t11, sT_, lane);
-        else if (wave == 2) l10 = lower_tile(sK, gs, lane);
-        else if (OUT && wave == 3) qk_tiles(sQ, sK, gs, sA, lane);
-        __syncthreads();
-        if (wave == 2) off_diagonal(l10, t00, t11, gs, sT_, lane);
-        __syncthreads();
-        if (chain) {
-            f32x4 o[2][NT];
-            chunk_step<NT, OUT>(sQ, sK, sV, sT_, sA, gs, col0, lane, st, o);
-            if constexpr (OUT) {
-                const auto rsrc = chunk_rsrc(ob + (size_t)ci * GC * st_v, (uint32_t)nrows * st_v);
-#pragma unroll
-                for (int rt = 0; rt < 2; ++rt)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const f32x4 x = a.scale * o[rt][n];
-                        __builtin_amdgcn_raw_buffer_store_b64(pack4(x), rsrc,
-                                                              (int)((16 * rt + m) * st_v + (col0 + 16 * n + 4 * gg) * 2),
-                                                              0, 0);
-                    }
-            }
+
+    // wavefronts 4 .. 7: the state, 32 value columns each
+    const int col0 = 32 * (wave - 4);
+    // tile (0, 1) of every operand record
+    for (int i = (wave - 4) * 64 + lane; i < N_REC * 2 * 64; i += 256) {
+        const int slot = i >> 7, at = 2048 + (i >> 6 & 1) * 1024 + (32 * (i >> 4 & 1) + (i & 15)) * 16;
+        if (!(i >> 5 & 1)) {
+            *(u32x4*)(lds.t[slot] + at) = u32x4{0, 0, 0, 0};
+            if constexpr (OUT) *(u32x4*)(lds.a[slot] + at) = u32x4{0, 0, 0, 0};
         }
     }
-    if (chain && (un.out >= 0 || (un.out == GD_FINAL && a.sT))) {
-        const bool b16 = un.out < 0 && a.state_bf16;
-        const int64_t base = ((int64_t)(un.out >= 0 ? un.out : un.seq) * a.H + h) * (D * D);
-        float* f = un.out >= 0 ? a.sums : (float*)a.sT;
+    f32x16 S[4];
+    // the element of the 128 x 128 state that element 4a + b of tile t is on this lane
+    const int at0 = 8 * (lane >> 5) * D + col0 + value_col(lane & 31);
+    auto each = [&](auto f) __attribute__((always_inline)) {
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int i = 0; i < 16; ++i)
+                S[t][i] = f(at0 + (32 * t + 16 * (i >> 3) + (i & 7)) * D, S[t][i]);
+    };
+    const int64_t own = ((int64_t)un.seq * a.H + h) * (D * D);
+    if (un.in >= 0) {
+        const float* p = a.carries + ((int64_t)un.in * a.H + h) * (D * D);
+        each([&](int at, float) { return p[at]; });
+    } else if (un.in == GD_INITIAL && a.s0) {
+        if (a.state_bf16) {
+            const uint16_t* p = (const uint16_t*)a.s0 + own;
+            each([&](int at, float) { return __uint_as_float((uint32_t)p[at] << 16); });
+        } else {
+            const float* p = (const float*)a.s0 + own;
+            each([&](int at, float) { return p[at]; });
+        }
+    } else {
+        const float one = un.in == GD_IDENTITY ? 1.f : 0.f;
+        each([&](int at, float) { return at % (D + 1) == 0 ? one : 0.f; });
+    }
+    for (int i = -DEPTH; i < 0; ++i) lds_barrier();
+    uint8_t* ob = (uint8_t*)a.out + (beg * a.H + h) * (D * 2);
+    Ring<N_QK> qk;
+    Ring<N_V> rv;
+    Ring<N_REC> rec;
+    Ring<N_GS> gs;
+    for (int i = 0; i < DEPTH; ++i) {
+        qk.next();
+        rv.next();
+        rec.next();
+        gs.next();
+    }
+    const MinusOne neg = minus_one(lane);
+    Rest rest = {};
+    // the output rows of chunk i (none before the first)
+    auto store = [&](int i, const f32x16& o) __attribute__((always_inline)) {
+        const auto rsrc = chunk_rsrc(ob + (size_t)(i < 0 ? 0 : i) * GC * st_v, (uint32_t)rows_of_chunk(n_tok, i) * st_v);
+        const int at = (int)((lane & 31) * st_v) + (col0 + 16 * (lane >> 5)) * 2;
 #pragma unroll
-                for (int v = 0; v < 4; ++v) {
-                    const int64_t i = base + state_channel(t, gg, v) * D + col0 + 16 * n + m;
-                    if (b16) ((uint16_t*)a.sT)[i] = (uint16_t)pack_bf16(st.s[t][n][v], 0.f);
-                    else f[i] = st.s[t][n][v];
-                }
+        for (int j = 0; j < 2; ++j) {
+            const u32x2 x = pack4(quarter(o, 2 * j)), y = pack4(quarter(o, 2 * j + 1));
+            __builtin_amdgcn_raw_buffer_store_b128(u32x4{x.x, x.y, y.x, y.y}, rsrc, at + 16 * j, 0, 0);
+        }
+    };
+    for (int i = 0; i < n_chunks; ++i) {
+        chunk_step<OUT>(lds.q[OUT ? qk.at[0] : 0], lds.k[qk.at[0]], lds.v[rv.at[0]], lds.t[rec.at[0]],
+                        lds.a[OUT ? rec.at[0] : 0], lds.gs[gs.at[0]], a.scale, col0, lane, neg, S, rest,
+                        [&](const f32x16& o) __attribute__((always_inline)) { store(i - 1, o); });
+        lds_barrier();
+        qk.next();
+        rv.next();
+        rec.next();
+        gs.next();
+    }
+    if constexpr (OUT) {
+        finish_output(rest);
+        store(n_chunks - 1, rest.o);
+    }
+    if (un.out >= 0) {
+        float* p = a.sums + ((int64_t)un.out * a.H + h) * (D * D);
+        each([&](int at, float s) { return p[at] = s; });
+    } else if (un.out == GD_FINAL && a.sT) {
+        if (a.state_bf16) {
+            uint16_t* p = (uint16_t*)a.sT + own;
+            each([&](int at, float s) {
+                p[at] = (uint16_t)pack_bf16(s, 0.f);
+                return s;
+            });
+        } else {
+            float* p = (float*)a.sT + own;
+            each([&](int at, float s) { return p[at] = s; });
+        }
     }
 }
 
@@ -596,12 +885,31 @@ __global__ __launch_bounds__(64 * DEC_W) void gd_decode(GdDecodeArgs a) {
 
 }  // namespace
 
+template <bool OUT>
+hipError_t run_gd_prefill(const GdArgs& a, hipStream_t s) {
+    // more LDS than the default limit, allowed once per device and process
+    static std::mutex mu;
+    static uint64_t done[4] = {0, 0, 0, 0};
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        if (dev >= 256 || !(done[dev >> 6] >> (dev & 63) & 1)) {
+            e = hipFuncSetAttribute((const void*)gd_prefill<OUT>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)sizeof(Lds<OUT>));
+            if (e != hipSuccess) return e;
+            if (dev < 256) done[dev >> 6] |= 1ull << (dev & 63);
+        }
+    }
+    const dim3 grid((unsigned)(a.n_units * a.H)), block(512);
+    hipLaunchKernelGGL((gd_prefill<OUT>), grid, block, sizeof(Lds<OUT>), s, a);
+    return hipGetLastError();
+}
+
 hipError_t launch_gd_prefill(const GdArgs& a, bool with_out, hipStream_t s) {
     if (a.n_units == 0) return hipSuccess;
-    const dim3 grid((unsigned)(a.n_units * a.H)), block(512);
-    if (with_out) hipLaunchKernelGGL((gd_prefill<2, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((gd_prefill<2, false>), grid, block, 0, s, a);
-    return hipGetLastError();
+    return with_out ? run_gd_prefill<true>(a, s) : run_gd_prefill<false>(a, s);
 }
 
 hipError_t launch_gd_merge(const GdMergeArgs& a, hipStream_t s) {
