@@ -4,7 +4,9 @@
 #include <climits>
 #include <cmath>
 #include <cstring>
+#include <functional>
 #include <new>
+#include <queue>
 
 #include "gated_delta_launch.h"
 #include "kda_internal.h"
@@ -15,23 +17,35 @@ namespace {
 
 constexpr int32_t kMaxHeads = 1 << 17;  // 32 token rows of one tensor stay below 2^31 bytes
 
-// Cost model of a plan, microseconds on MI355X: one chunk of a unit with
-// output, one chunk without (a segment's end state or transfer), one merge
-// step, and one launch.
-constexpr double kFullUs = 2.0, kPreUs = 1.6, kMergeUs = 2.5, kLaunchUs = 6.0;
+// Cost model of a plan, microseconds on MI355X, fitted to launches of 8 to 2048
+// units of 8 to 2048 chunks: a chunk of a unit with output, one without (a
+// segment's end state or transfer), what a launch of either takes beside its
+// chunks, a merge step and the rest of a merge.
+constexpr double kFullUs = 1.75, kPreUs = 1.55, kUnitUs = 7.0, kMergeUs = 1.6, kMergeLaunchUs = 5.0;
 
-// A launch of units of these chunk counts, H heads each, over the CUs: the
-// longest unit, or all work spread evenly.
-double launch_us(const std::vector<int>& chunks, int H, int n_cus, double per_chunk) {
+// A launch of units of these chunk counts (longest first), H heads each: one
+// workgroup per compute unit, the next one to whichever is free first.
+double launch_us(std::vector<int> chunks, int H, int n_cus, double per_chunk) {
+    if (chunks.empty()) return 0;
+    std::sort(chunks.begin(), chunks.end(), std::greater<int>());
+    const int64_t n = (int64_t)chunks.size() * H;
     double total = 0;
-    int longest = 0;
-    for (int c : chunks) {
-        total += c;
-        longest = std::max(longest, c);
-    }
-    const double rounds = std::ceil((double)chunks.size() * H / n_cus);
-    const double even = total * H / n_cus;
-    return per_chunk * std::max({(double)longest, even, rounds > 1 ? even : 0.0});
+    for (int c : chunks) total += (double)c * H;
+    if (n > 16384) return kUnitUs + per_chunk * std::max((double)chunks[0], total / n_cus + chunks[0]);
+    std::priority_queue<double, std::vector<double>, std::greater<double>> busy;
+    double end = 0;
+    for (int c : chunks)
+        for (int h = 0; h < H; ++h) {
+            double t = 0;
+            if ((int)busy.size() == n_cus) {
+                t = busy.top();
+                busy.pop();
+            }
+            t += kUnitUs + per_chunk * c;
+            busy.push(t);
+            end = std::max(end, t);
+        }
+    return end;
 }
 
 int segments_of(int chunks, int seg) { return seg > 0 && chunks > seg ? (chunks + seg - 1) / seg : 1; }
@@ -50,7 +64,7 @@ double plan_us(const std::vector<int>& nch, int H, int n_cus, int seg) {
         }
     }
     double us = launch_us(main, H, n_cus, kFullUs);
-    if (most > 1) us += launch_us(pre, H, n_cus, kPreUs) + (most - 2) * kMergeUs + 2 * kLaunchUs;
+    if (most > 1) us += launch_us(pre, H, n_cus, kPreUs) + (most - 2) * kMergeUs + kMergeLaunchUs;
     return us;
 }
 
