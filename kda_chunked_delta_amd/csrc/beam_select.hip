@@ -36,13 +36,19 @@ __device__ __forceinline__ float clean(float x) { return x != x ? NEG_INF : x + 
 // A key orders by logit, then by lower token; 0 is no candidate.
 __device__ __forceinline__ uint64_t key_of(uint32_t s, uint32_t token) { return (uint64_t)s << 32 | ~token; }
 
+__device__ __forceinline__ void set16(u32x4& v, int j, uint32_t x) {
+    v[j >> 1] = j & 1 ? (v[j >> 1] & 0xffffu) | x << 16 : x;
+}
+
 template <int DT>
 struct Elem;
 template <>
 struct Elem<KDA_FP32> {
     static constexpr int SIZE = 4;
+    static constexpr uint32_t NONE = 0xff800000u;  // -inf
     static __device__ __forceinline__ float get(const u32x4& v, int j) { return __uint_as_float(v[j]); }
-    static __device__ __forceinline__ float at(const void* p, int64_t i) { return ((const float*)p)[i]; }
+    static __device__ __forceinline__ void set(u32x4& v, int j, uint32_t x) { v[j] = x; }
+    static __device__ __forceinline__ uint32_t raw(const void* p, int64_t i) { return ((const uint32_t*)p)[i]; }
 };
 template <>
 struct Elem<KDA_BF16> {
@@ -50,9 +56,9 @@ struct Elem<KDA_BF16> {
     static __device__ __forceinline__ float get(const u32x4& v, int j) {
         return __uint_as_float(j & 1 ? v[j >> 1] & 0xffff0000u : v[j >> 1] << 16);
     }
-    static __device__ __forceinline__ float at(const void* p, int64_t i) {
-        return __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16);
-    }
+    static constexpr uint32_t NONE = 0xff80u;
+    static __device__ __forceinline__ void set(u32x4& v, int j, uint32_t x) { set16(v, j, x); }
+    static __device__ __forceinline__ uint32_t raw(const void* p, int64_t i) { return ((const uint16_t*)p)[i]; }
 };
 template <>
 struct Elem<KDA_FP16> {
@@ -63,16 +69,14 @@ struct Elem<KDA_FP16> {
     static __device__ __forceinline__ float get(const u32x4& v, int j) {
         return half(j & 1 ? v[j >> 1] >> 16 : v[j >> 1] & 0xffffu);
     }
-    static __device__ __forceinline__ float at(const void* p, int64_t i) { return half(((const uint16_t*)p)[i]); }
+    static constexpr uint32_t NONE = 0xfc00u;
+    static __device__ __forceinline__ void set(u32x4& v, int j, uint32_t x) { set16(v, j, x); }
+    static __device__ __forceinline__ uint32_t raw(const void* p, int64_t i) { return ((const uint16_t*)p)[i]; }
 };
 
-template <class T>
-__device__ __forceinline__ T wave_max(T x) {
+__device__ __forceinline__ float wave_max(float x) {
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const T y = __shfl_xor(x, d, 64);
-        x = y > x ? y : x;
-    }
+    for (int d = 1; d < 64; d <<= 1) x = fmaxf(x, __shfl_xor(x, d, 64));
     return x;
 }
 
@@ -84,16 +88,54 @@ __device__ __forceinline__ u32x4 load16(const uint8_t* p) {
     return v;
 }
 
-// VECS 16-byte vectors per thread. A chunk's elements and the order of its sums
-// depend on the row's length alone, not on its address: equal rows get equal
-// sums, and their candidates tie. exp(x - m) is exp2 of (x - m) log2(e) with
-// the product's rounding put back in, added in pairs and then in fp64, which
-// leaves exp2's own last bit (2^-23) and one rounding (2^-24) at most.
+// The n-th largest key of a wavefront's 64 (n <= 64; keys differ, or are 0):
+// the value bit by bit from ballots, then the token among the lanes that hold
+// that value.
+__device__ __forceinline__ uint64_t nth_key(uint32_t value, uint32_t token, int n) {
+    uint32_t v = 0;
+#pragma unroll
+    for (int b = 31; b >= 0; --b) {
+        const uint32_t c = v | 1u << b;
+        v = __popcll(__ballot(value >= c)) >= n ? c : v;
+    }
+    if (v == 0) return 0;
+    uint64_t tied = __ballot(value == v);
+    int left = n - __popcll(__ballot(value > v));  // how many of the tied ones count
+    uint32_t t = 0;
+    while (left-- > 0) {
+        uint32_t low = tied >> (threadIdx.x & 63) & 1 ? token : 0xffffffffu;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const uint32_t o = __shfl_xor(low, d, 64);
+            low = o < low ? o : low;
+        }
+        t = low;
+        tied &= ~__ballot(token == low && (tied >> (threadIdx.x & 63) & 1));
+    }
+    return key_of(v, t);
+}
+
+// One workgroup of 256 threads per chunk of a row, N elements per thread in
+// VECS 16-byte vectors.
+//
+// Sums. A chunk's elements and the order of its sums depend on the row's
+// length alone, not on its address: equal rows get equal sums, and their
+// candidates tie. exp(x - m) is exp2 of (x - m) log2(e) with the product's
+// rounding put back in, added in pairs and then in fp64, which leaves exp2's
+// own last bit (2^-23) and one rounding (2^-24) at most.
+//
+// Keys. The 256 threads form 64 groups of 4 (one lane of each wavefront). The
+// n-th largest of the groups' first keys is a lower edge of the chunk's n first
+// keys, and only n groups have keys at or above it: those (at most 4 n N, in
+// practice little more than n) are ranked by counting.
+//
+// Measured on 32 x 8 rows of 131072 bf16 logits, n = 16 (67 MB): 71 us with
+// the edge from ranks over all 256 threads' first keys, which took most of it.
 template <int DT, int VECS>
 __global__ __launch_bounds__(256) void beam_rows(BeamArgs a) {
     constexpr int PER = 16 / Elem<DT>::SIZE, N = VECS * PER;
-    __shared__ uint64_t s_key[256];
-    __shared__ uint64_t s_cand[kBeamPickMax * N];
+    extern __shared__ uint64_t s_cand[];  // [4 n N]
+    __shared__ uint32_t s_value[4][64], s_token[4][64];
     __shared__ float s_max[4];
     __shared__ double s_sum[4];
     __shared__ uint64_t s_edge;
@@ -103,77 +145,94 @@ __global__ __launch_bounds__(256) void beam_rows(BeamArgs a) {
     const int64_t row = blockIdx.x / a.splits;
     if (a.finished && a.finished[row]) return;
     const uint8_t* base = (const uint8_t*)a.logits + row * a.row_stride * Elem<DT>::SIZE;
-    const int first = split * a.chunk;
-    float x[N];
-    uint32_t best_s = 0, best_t = 0;
-    float m = NEG_INF;
-    if (tid == 0) s_count = 0;
-    bool any = false;
+    const int first = split * a.chunk + tid * PER;  // vector i starts at first + 256 PER i
+    u32x4 x[VECS];
 #pragma unroll
     for (int i = 0; i < VECS; ++i) {
-        const int t0 = first + (i * 256 + tid) * PER;
-        u32x4 v = {0, 0, 0, 0};
-        const bool whole = t0 + PER <= a.vocab;
-        if (whole) v = load16<DT>(base + (int64_t)t0 * Elem<DT>::SIZE);
+        const int t0 = first + i * 256 * PER;
+        if (t0 + PER <= a.vocab) {
+            x[i] = load16<DT>(base + (int64_t)t0 * Elem<DT>::SIZE);
+        } else {
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-            const int t = t0 + j;
-            float y = NEG_INF;
-            if (whole) y = clean(Elem<DT>::get(v, j));
-            else if (t < a.vocab) y = clean(Elem<DT>::at(base, t));
-            x[i * PER + j] = y;
-            m = y > m ? y : m;
-            const uint32_t s = sortable(y);
-            if (t < a.vocab && (!any || s > best_s)) {
-                best_s = s;
-                best_t = (uint32_t)t;
-                any = true;
-            }
+            for (int j = 0; j < PER; ++j) Elem<DT>::set(x[i], j, t0 + j < a.vocab ? Elem<DT>::raw(base, t0 + j) : Elem<DT>::NONE);
         }
     }
-    const uint64_t mine = any ? key_of(best_s, best_t) : 0;
-    m = wave_max(m);
-    if (lane == 0) s_max[wave] = m;
-    s_key[tid] = mine;
-    __syncthreads();
-    m = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
-    double sum = 0.0;
+    if (tid == 0) s_count = 0;
+    // the thread's first key: NaN never compares greater; all -inf leaves the first token
+    float best = NEG_INF;
+    int at = 0;
 #pragma unroll
     for (int i = 0; i < VECS; ++i)
 #pragma unroll
-        for (int j = 0; j < PER; j += 2) {
-            float e[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const float y = x[i * PER + j + u], d = y - m;
-                const float hi = d * LOG2E;
-                const float lo = __builtin_fmaf(d, LOG2E, -hi) + d * LOG2E_LO;
-                const float p = __builtin_amdgcn_exp2f(hi);
-                // exp2 of a large negative number is 0, and y - m is 0 - 0 or
-                // inf - inf where both are the maximum: that counts as 1
-                e[u] = y == m ? 1.f : p > 0.f ? __builtin_fmaf(p, lo * LN2, p) : 0.f;
-                if (first + (i * 256 + tid) * PER + j + u >= a.vocab) e[u] = 0.f;
+        for (int j = 0; j < PER; ++j) {
+            const float y = Elem<DT>::get(x[i], j);
+            if (y > best) {
+                best = y;
+                at = i * 256 * PER + j;
             }
-            sum += (double)(e[0] + e[1]);
         }
+    const bool any = first < a.vocab;
+    s_value[wave][lane] = any ? sortable(best + 0.0f) : 0u;
+    s_token[wave][lane] = (uint32_t)(first + at);
+    const float wm = wave_max(best);
+    if (lane == 0) s_max[wave] = wm;
+    __syncthreads();
+    if (wave == 0) {
+        uint32_t v = s_value[0][lane], t = s_token[0][lane];
+#pragma unroll
+        for (int w = 1; w < 4; ++w) {
+            const uint32_t ov = s_value[w][lane], ot = s_token[w][lane];
+            if (ov > v || (ov == v && ot < t)) {
+                v = ov;
+                t = ot;
+            }
+        }
+        const uint64_t edge = nth_key(v, t, a.n);
+        if (lane == 0) s_edge = edge;
+    }
+    const float m = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
+    double sum = 0.0;
+    if (__builtin_isinf(m)) {  // no logit above -inf: all count as 1; or some at +inf, which share the row
+#pragma unroll
+        for (int i = 0; i < VECS; ++i)
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                if (first + i * 256 * PER + j < a.vocab && Elem<DT>::get(x[i], j) == m) sum += 1.0;
+    } else {
+#pragma unroll
+        for (int i = 0; i < VECS; ++i)
+#pragma unroll
+            for (int j = 0; j < PER; j += 2) {
+                float e[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    // -inf and NaN become -200, whose exponential is 0
+                    const float d = fmaxf(Elem<DT>::get(x[i], j + u) - m, -200.f);
+                    const float hi = d * LOG2E;
+                    const float lo = __builtin_fmaf(d, LOG2E_LO, __builtin_fmaf(d, LOG2E, -hi));
+                    const float p = __builtin_amdgcn_exp2f(hi);
+                    e[u] = __builtin_fmaf(p, lo * LN2, p);
+                }
+                sum += (double)(e[0] + e[1]);
+            }
+    }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d, 64);
     if (lane == 0) s_sum[wave] = sum;
-    // the n-th of the threads' first keys: the chunk's n first keys are at or
-    // above it, and only n threads have keys there
-    int rank = 0;
-    for (int i = 0; i < 256; ++i) rank += s_key[i] > mine || (s_key[i] == mine && i < tid);
-    if (rank == a.n - 1) s_edge = mine;
     __syncthreads();
     const uint64_t edge = s_edge;
-    if (mine >= edge && mine != 0)
+    const float edge_value = edge ? unsortable((uint32_t)(edge >> 32)) : NEG_INF;
+    if (any && best >= edge_value)
 #pragma unroll
         for (int i = 0; i < VECS; ++i)
 #pragma unroll
             for (int j = 0; j < PER; ++j) {
-                const int t = first + (i * 256 + tid) * PER + j;
-                const uint64_t k = key_of(sortable(x[i * PER + j]), (uint32_t)t);
-                if (t < a.vocab && k >= edge) s_cand[atomicAdd(&s_count, 1)] = k;
+                const float y = clean(Elem<DT>::get(x[i], j));
+                const int t = first + i * 256 * PER + j;
+                if (y >= edge_value && t < a.vocab) {
+                    const uint64_t k = key_of(sortable(y), (uint32_t)t);
+                    if (k >= edge) s_cand[atomicAdd(&s_count, 1)] = k;
+                }
             }
     __syncthreads();
     const int count = s_count;
@@ -207,43 +266,57 @@ __device__ __forceinline__ bool before(const Cand& x, const Cand& y) {
 // What a row adds to its logits.
 constexpr int ROW_PLAIN = 0, ROW_EMPTY = 1, ROW_FINISHED = 2;
 
-// Keys of a batch entry that are staged in LDS (48 KiB); larger entries are
-// read from memory.
-constexpr int PICK_LDS_KEYS = 6144;
+// Keys of a batch entry that are staged in LDS, and lists that a lane then keeps
+// the heads of in registers; larger entries are read from memory.
+constexpr int PICK_LDS_KEYS = 6144, PICK_LANE_LISTS = 4;
 
-// One wavefront per batch entry. A row is `splits` sorted lists, or one list
+// The larger of two unsigned numbers over the wavefront, by DPP.
+__device__ __forceinline__ uint32_t wave_umax(uint32_t x) {
+#define KDA_UMAX(CTRL)                                                                               \
+    {                                                                                                \
+        const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xF, 0xF, false); \
+        x = o > x ? o : x;                                                                           \
+    }
+    KDA_UMAX(0x111) KDA_UMAX(0x112) KDA_UMAX(0x114) KDA_UMAX(0x118) KDA_UMAX(0x142) KDA_UMAX(0x143)
+#undef KDA_UMAX
+    return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
+}
+
+// One workgroup per batch entry. A row is `splits` sorted lists, or one list
 // made up on the spot: a finished beam's end token and then -inf, or -inf
-// throughout (no logit or score above -inf). Each lane keeps the best head of
-// its lists; a round takes the best of the lanes, and its owner moves on.
+// throughout (no logit or score above -inf). All wavefronts stage the keys;
+// then the first selects: each lane keeps the heads of its lists, a round takes
+// the best of them (by the upper half of the value's bits, which is nearly
+// always enough), and its owner moves on. Bound by the latency of n such rounds
+// (measured: 1.1 us each with the heads looked up anew, n = 16, 128 lists).
 template <bool STAGED>
-__global__ __launch_bounds__(64) void beam_pick(BeamArgs a) {
+__global__ __launch_bounds__(256) void beam_pick(BeamArgs a) {
     __shared__ double s_log[kBeamMax];
     __shared__ float s_top[kBeamMax], s_score[kBeamMax];
     __shared__ int s_kind[kBeamMax];
     __shared__ uint64_t s_keys[STAGED ? PICK_LDS_KEYS : 1];
     extern __shared__ uint16_t s_pos[];  // [beams * splits] entries taken of each list
-    const int lane = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 63;
     const int64_t row0 = (int64_t)blockIdx.x * a.beams;
     const int lists = a.beams * a.splits;
     const uint64_t* keys = a.keys + row0 * a.splits * a.n;
     if constexpr (STAGED)
-        for (int i = lane; i < lists * a.n; i += 64) s_keys[i] = keys[i];
-    // maximum and sum of the rows: `span` lanes (a power of two) per row
-    const int span = a.beams > 32 ? 1 : a.beams > 16 ? 2 : a.beams > 8 ? 4 : a.beams > 4 ? 8 : 16;
+        for (int i = tid; i < lists * a.n; i += 256) s_keys[i] = keys[i];
+    // maximum and sum of the rows: 4 lanes per row
     {
-        const int w = lane / span, sub = lane % span;
+        const int w = tid >> 2, sub = tid & 3;
         const bool row = w < a.beams && !(a.finished && a.finished[row0 + w]);
         const float* mx = a.maxima + (row0 + w) * a.splits;
         const double* sm = a.sums + (row0 + w) * a.splits;
         float top = NEG_INF;
         if (row)
-            for (int i = sub; i < a.splits; i += span) top = mx[i] > top ? mx[i] : top;
-        for (int d = 1; d < span; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+            for (int i = sub; i < a.splits; i += 4) top = mx[i] > top ? mx[i] : top;
+        for (int d = 1; d < 4; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
         double sum = 0;
         if (row)
-            for (int i = sub; i < a.splits; i += span)
+            for (int i = sub; i < a.splits; i += 4)
                 sum += mx[i] == top ? sm[i] : sm[i] * exp((double)mx[i] - (double)top);
-        for (int d = 1; d < span; d <<= 1) sum += __shfl_xor(sum, d, 64);
+        for (int d = 1; d < 4; d <<= 1) sum += __shfl_xor(sum, d, 64);
         if (w < a.beams && sub == 0) {
             const float sc = clean(a.scores[row0 + w]);
             s_kind[w] = !row ? ROW_FINISHED : top == NEG_INF || sc == NEG_INF ? ROW_EMPTY : ROW_PLAIN;
@@ -252,79 +325,101 @@ __global__ __launch_bounds__(64) void beam_pick(BeamArgs a) {
             s_log[w] = log(sum);
         }
     }
-    for (int l = lane; l < lists; l += 64) s_pos[l] = 0;
+    if constexpr (!STAGED)
+        for (int l = tid; l < lists; l += 256) s_pos[l] = 0;
     __syncthreads();
+    if (tid >= 64) return;
     const double none = -__builtin_huge_val();
-    auto head = [&](int l) {
-        const int w = l / a.splits, pos = s_pos[l];
+    // entry `pos` of list l, which belongs to beam w: its key (0: none) and value
+    auto entry = [&](int l, int w, int pos, bool first_list) __attribute__((always_inline)) {
         Cand c{none, NO_BEAM, 0};
         const int kind = s_kind[w];
+        const float sc = s_score[w];
         if (kind == ROW_PLAIN) {
-            const uint64_t k = pos < a.n ? (STAGED ? s_keys[l * a.n + pos] : keys[(int64_t)l * a.n + pos]) : 0;
-            if (k) {
-                const float x = unsortable((uint32_t)(k >> 32)), top = s_top[w];
-                c.beam = w;
-                c.key = k;
-                if (x > NEG_INF) c.v = (x == top ? 0.0 : (double)x - (double)top) - s_log[w] + (double)s_score[w];
-                if (c.v != c.v) c.v = none;  // no probability, at a score of +inf
+            c.key = pos < a.n ? (STAGED ? s_keys[l * a.n + pos] : keys[(int64_t)l * a.n + pos]) : 0;
+            const float x = unsortable((uint32_t)(c.key >> 32)), top = s_top[w];
+            if (c.key && x > NEG_INF) {
+                const double v = (x == top ? 0.0 : (double)x - (double)top) - s_log[w] + (double)sc;
+                c.v = v == v ? v + 0.0 : none;  // NaN: no probability, at a score of +inf
             }
-        } else if (l % a.splits == 0) {
-            const float sc = s_score[w];
+        } else if (first_list) {
             // a finished beam's end token leads, unless it is itself at -inf: then its place is that of its index
             const bool lead = kind == ROW_FINISHED && sc > NEG_INF;
             const int t = !lead ? pos : pos == 0 ? a.eos : pos - 1 < a.eos ? pos - 1 : pos;
-            if (t < a.vocab) {
-                c.beam = w;
-                c.key = key_of(sortable(lead && pos == 0 ? 0.f : NEG_INF), (uint32_t)t);
-                if (lead && pos == 0) c.v = sc;
-            }
+            if (t < a.vocab) c.key = key_of(sortable(lead && pos == 0 ? 0.f : NEG_INF), (uint32_t)t);
+            if (lead && pos == 0) c.v = (double)sc + 0.0;
         }
+        if (c.key) c.beam = (uint32_t)w;
         return c;
     };
     Cand best;
     int from;
-    auto rescan = [&] {
+    // the lane's lists lane + 64q
+    Cand head[PICK_LANE_LISTS];
+    int pos[PICK_LANE_LISTS], beam[PICK_LANE_LISTS];
+    auto choose = [&]() __attribute__((always_inline)) {
         best = Cand{none, NO_BEAM, 0};
         from = 0;
-        for (int l = lane; l < lists; l += 64) {
-            const Cand c = head(l);
-            if (before(c, best)) {
-                best = c;
-                from = l;
+        if constexpr (STAGED) {
+#pragma unroll
+            for (int q = 0; q < PICK_LANE_LISTS; ++q)
+                if (before(head[q], best)) {
+                    best = head[q];
+                    from = q;
+                }
+        } else {
+            for (int l = lane; l < lists; l += 64) {
+                const Cand c = entry(l, l / a.splits, s_pos[l], l % a.splits == 0);
+                if (before(c, best)) {
+                    best = c;
+                    from = l;
+                }
             }
         }
     };
-    rescan();
-    for (int i = 0; i < a.n; ++i) {
-        double top = best.v;
+    if constexpr (STAGED) {
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) top = fmax(top, __shfl_xor(top, d, 64));
-        uint64_t at = __ballot(best.v == top && best.beam != NO_BEAM);
-        if (at & (at - 1)) {  // equal values: compare the rest
-            Cand w = best.v == top ? best : Cand{none, NO_BEAM, 0};
-            uint32_t beam = w.beam;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const uint32_t o = __shfl_xor(beam, d, 64);
-                beam = o < beam ? o : beam;
-            }
-            uint64_t key = w.beam == beam ? w.key : 0;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const uint64_t o = __shfl_xor((unsigned long long)key, d, 64);
-                key = o > key ? o : key;
-            }
-            at = __ballot(best.v == top && best.beam == beam && best.key == key);
+        for (int q = 0; q < PICK_LANE_LISTS; ++q) {
+            const int l = lane + 64 * q;
+            pos[q] = 0;
+            beam[q] = l < lists ? l / a.splits : 0;
+            head[q] = l < lists ? entry(l, beam[q], 0, l == beam[q] * a.splits) : Cand{none, NO_BEAM, 0};
         }
-        if (at >> lane & 1) {
+    }
+    choose();
+    for (int i = 0; i < a.n; ++i) {
+        const uint64_t bits = __builtin_bit_cast(uint64_t, best.v);
+        const uint64_t order = best.beam == NO_BEAM ? 0 : bits ^ (bits >> 63 ? ~0ull : 1ull << 63);
+        const uint32_t hi = wave_umax((uint32_t)(order >> 32));
+        uint64_t at = __ballot((uint32_t)(order >> 32) == hi);
+        if (at & (at - 1)) {  // the rest of the value, then beam and key
+            const uint32_t lo = wave_umax(at >> lane & 1 ? (uint32_t)order : 0u);
+            at = __ballot((at >> lane & 1) && (uint32_t)order == lo);
+            const uint32_t beam = ~wave_umax(at >> lane & 1 ? ~best.beam : 0u);
+            at = __ballot((at >> lane & 1) && best.beam == beam);
+            const uint32_t k1 = wave_umax(at >> lane & 1 ? (uint32_t)(best.key >> 32) : 0u);
+            at = __ballot((at >> lane & 1) && (uint32_t)(best.key >> 32) == k1);
+            const uint32_t k0 = wave_umax(at >> lane & 1 ? (uint32_t)best.key : 0u);
+            at = __ballot((at >> lane & 1) && (uint32_t)best.key == k0);
+        }
+        if (at >> lane & 1 && best.beam != NO_BEAM) {
             const int64_t o = (int64_t)blockIdx.x * a.n + i;
             const int32_t token = (int32_t)~(uint32_t)best.key;
             a.out_scores[o] = (float)best.v;
             a.out_parents[o] = (int32_t)best.beam;
             a.out_tokens[o] = token;
             if (a.out_finished) a.out_finished[o] = token == a.eos || s_kind[best.beam] == ROW_FINISHED;
-            s_pos[from] += 1;
-            rescan();
+            if constexpr (STAGED) {
+#pragma unroll
+                for (int q = 0; q < PICK_LANE_LISTS; ++q)
+                    if (q == from) {
+                        const int l = lane + 64 * q;
+                        head[q] = entry(l, beam[q], ++pos[q], l == beam[q] * a.splits);
+                    }
+            } else {
+                s_pos[from] += 1;
+            }
+            choose();
         }
     }
 }
@@ -334,8 +429,9 @@ hipError_t rows(const BeamArgs& a, hipStream_t s) {
     const dim3 grid((unsigned)((int64_t)a.batch * a.beams * a.splits)), block(256);
     constexpr int PER = 16 / Elem<DT>::SIZE;
     const int vecs = a.chunk / (256 * PER);
-    if (vecs * PER == 32) hipLaunchKernelGGL((beam_rows<DT, 32 / PER>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((beam_rows<DT, 8 / PER>), grid, block, 0, s, a);
+    const size_t lds = (size_t)4 * a.n * vecs * PER * sizeof(uint64_t);
+    if (vecs * PER == 32) hipLaunchKernelGGL((beam_rows<DT, 32 / PER>), grid, block, lds, s, a);
+    else hipLaunchKernelGGL((beam_rows<DT, 8 / PER>), grid, block, lds, s, a);
     return hipGetLastError();
 }
 
@@ -348,9 +444,10 @@ hipError_t launch_beam_rows(const BeamArgs& a, int dtype, hipStream_t s) {
 }
 
 hipError_t launch_beam_pick(const BeamArgs& a, hipStream_t s) {
-    const dim3 grid((unsigned)a.batch), block(64);
+    const dim3 grid((unsigned)a.batch), block(256);
     const int64_t lists = (int64_t)a.beams * a.splits;
-    if (lists * a.n <= PICK_LDS_KEYS) hipLaunchKernelGGL(beam_pick<true>, grid, block, (size_t)lists * 2, s, a);
+    if (lists * a.n <= PICK_LDS_KEYS && lists <= 64 * PICK_LANE_LISTS)
+        hipLaunchKernelGGL(beam_pick<true>, grid, block, 0, s, a);
     else hipLaunchKernelGGL(beam_pick<false>, grid, block, (size_t)lists * 2, s, a);
     return hipGetLastError();
 }

@@ -64,9 +64,10 @@ kda_status on_device(kda_ctx* ctx, hipStream_t stream, const char* who, F&& body
 }
 
 // Chunks of a row: 8192 elements per workgroup, or 2048 where that leaves the
-// chip with fewer than two workgroups per compute unit.
-void beam_split(int64_t rows, int64_t vocab, int32_t* chunk, int32_t* splits) {
-    *chunk = rows * ((vocab + 8191) / 8192) >= 512 ? 8192 : 2048;
+// chip with fewer than two workgroups per compute unit, or where the room for
+// a chunk's candidates (4 n per element and thread) would pass 32 KiB.
+void beam_split(int64_t rows, int64_t vocab, int32_t n, int32_t* chunk, int32_t* splits) {
+    *chunk = n <= 32 && rows * ((vocab + 8191) / 8192) >= 512 ? 8192 : 2048;
     *splits = (int32_t)((vocab + *chunk - 1) / *chunk);
 }
 
@@ -214,7 +215,7 @@ kda_status kda_beam_reorder(kda_ctx* ctx, const kda_pool* pool, const int32_t* s
 size_t kda_beam_select_workspace_bytes(int32_t batch, int32_t beams, int32_t vocab, int32_t n) {
     if (batch < 1 || beams < 1 || vocab < 1 || n < 1) return 0;
     int32_t chunk, splits;
-    beam_split((int64_t)batch * beams, vocab, &chunk, &splits);
+    beam_split((int64_t)batch * beams, vocab, n, &chunk, &splits);
     return (size_t)batch * beams * splits * ((size_t)n * 8 + 8 + 4);
 }
 
@@ -244,7 +245,7 @@ kda_status kda_beam_select_validate(int32_t batch, int32_t beams, int32_t vocab,
     if (batch == 0) return KDA_OK;
     const int64_t rows = (int64_t)batch * beams;
     int32_t chunk, splits;
-    beam_split(rows, vocab, &chunk, &splits);
+    beam_split(rows, vocab, n, &chunk, &splits);
     if (rows * splits > INT32_MAX || rows > INT32_MAX / 64 || (int64_t)beams * splits > 24 * 1024)
         return fail(KDA_ERR_INVALID, "%s: batch * beams * vocab too large", who);
     const size_t size = dtype == KDA_FP32 ? 4 : 2, R = (size_t)rows, K = (size_t)batch * n;
@@ -282,7 +283,7 @@ kda_status kda_beam_select(kda_ctx* ctx, int32_t batch, int32_t beams, int32_t v
                                                    workspace_bytes);
     if (st != KDA_OK || batch == 0) return st;
     BeamArgs a{logits, row_stride, scores, finished, eos, batch, beams, vocab, n};
-    beam_split((int64_t)batch * beams, vocab, &a.chunk, &a.splits);
+    beam_split((int64_t)batch * beams, vocab, n, &a.chunk, &a.splits);
     const size_t lists = (size_t)batch * beams * a.splits;
     a.keys = (uint64_t*)workspace;
     a.sums = (double*)(a.keys + lists * n);

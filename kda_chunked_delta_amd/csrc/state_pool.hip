@@ -42,11 +42,14 @@ __global__ __launch_bounds__(256) void pool_move(PoolView p, const int32_t* src,
 }
 
 // Copies as if every source were read before any destination is written: each
-// workgroup holds its part (`vecs` vectors) of every source page in registers,
-// 8 vectors per thread, before it writes. Of several pairs with one
-// destination the last wins.
+// workgroup holds its part (2^log_vecs vectors) of every source page in
+// registers, J vectors per thread, before it writes. Of several pairs with one
+// destination the last wins. Vectors that nothing is copied from are read from
+// the pool's first bytes, so that the loads need no branches (with them the
+// compiler spilled the vectors: 40 us for two pages of 2 MiB instead of 8).
+template <int J>
 __global__ __launch_bounds__(1024) void pool_copy(PoolView p, const int32_t* src, const int32_t* dst, int32_t n,
-                                                  int32_t parts, int32_t vecs) {
+                                                  int32_t parts, int32_t log_vecs) {
     __shared__ int32_t to[kPoolCopyMax], from[kPoolCopyMax];
     const int tid = threadIdx.x;
     int d = -1;
@@ -65,20 +68,23 @@ __global__ __launch_bounds__(1024) void pool_copy(PoolView p, const int32_t* src
     __syncthreads();
     const int layer = blockIdx.x / parts, part = blockIdx.x % parts;
     uint8_t* base = p.base + layer * p.layer_stride;
-    u32x4 x[8];
+    // vector f of the workgroup: pair f >> log_vecs, a row of consecutive vectors of its page
+    const int64_t first = (int64_t)part << log_vecs;
+    u32x4 x[J];
+    uint8_t* w[J];  // where it goes
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int f = tid + j * 1024, i = f / vecs;
-        const int64_t at = ((int64_t)part * vecs + f % vecs) * 16;
-        if (i < n && to[i] >= 0 && at < p.page_bytes) x[j] = *(const u32x4*)(base + from[i] * p.page_bytes + at);
+    for (int j = 0; j < J; ++j) {
+        const int f = tid + j * 1024, i = f >> log_vecs;
+        const int64_t at = (first + (f & ((1 << log_vecs) - 1))) * 16;
+        const int t = i < n ? to[i] : -1;
+        const bool ok = t >= 0 && at < p.page_bytes;
+        x[j] = *(const u32x4*)(ok ? base + from[i] * p.page_bytes + at : p.base);
+        w[j] = ok ? base + t * p.page_bytes + at : nullptr;
     }
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int f = tid + j * 1024, i = f / vecs;
-        const int64_t at = ((int64_t)part * vecs + f % vecs) * 16;
-        if (i < n && to[i] >= 0 && at < p.page_bytes) *(u32x4*)(base + to[i] * p.page_bytes + at) = x[j];
-    }
+    for (int j = 0; j < J; ++j)
+        if (w[j]) *(u32x4*)w[j] = x[j];
 }
 
 // Exclusive prefix sum of x over 1024 threads; `all` gets the total. s_sum:
@@ -260,11 +266,18 @@ hipError_t launch_pool_move(const PoolView& p, const int32_t* src, const int32_t
 }
 
 hipError_t launch_pool_copy(const PoolView& p, const int32_t* src, const int32_t* dst, int32_t n, hipStream_t s) {
-    int vecs = 256;  // vectors of a part: 4 KiB down to 128 bytes, n parts within 8 vectors of 1024 threads
-    while (vecs * n > 8 * 1024) vecs >>= 1;
-    const int64_t parts = (p.page_bytes / 16 + vecs - 1) / vecs;
-    hipLaunchKernelGGL(pool_copy, dim3((unsigned)(parts * p.n_layers)), dim3(1024), 0, s, p, src, dst, n, (int)parts,
-                       vecs);
+    // vectors of a part: 64 KiB down to 128 bytes, n parts within 8 vectors of
+    // 1024 threads, and a page in parts for every compute unit if it has them
+    int log_vecs = 12;
+    while (log_vecs > 3 && ((int64_t)n << log_vecs > 8 * 1024 ||
+                            ((p.page_bytes / 16 * p.n_layers) >> log_vecs) < 512))
+        --log_vecs;
+    const int64_t parts = ((p.page_bytes / 16 - 1) >> log_vecs) + 1;
+    const dim3 grid((unsigned)(parts * p.n_layers)), block(1024);
+    const int64_t vectors = (int64_t)n << log_vecs;
+    if (vectors <= 1024) hipLaunchKernelGGL(pool_copy<1>, grid, block, 0, s, p, src, dst, n, (int)parts, log_vecs);
+    else if (vectors <= 4096) hipLaunchKernelGGL(pool_copy<4>, grid, block, 0, s, p, src, dst, n, (int)parts, log_vecs);
+    else hipLaunchKernelGGL(pool_copy<8>, grid, block, 0, s, p, src, dst, n, (int)parts, log_vecs);
     return hipGetLastError();
 }
 
