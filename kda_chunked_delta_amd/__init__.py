@@ -562,15 +562,24 @@ def plan_gated_delta_host(cu_seqlens, H, n_cus, use_intracard_cp="auto", seg_chu
 
 
 def _need(name, t, dtype, shape, device):
-    """Raise unless t is a contiguous tensor of this type, shape and device."""
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device or device.type != "cuda":
-        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s, a CUDA device (got %s %s on %s, strides "
-                         "%s)" % (name, dtype, tuple(shape), device, t.dtype, tuple(t.shape), t.device, t.stride()))
+    """Raise unless t is a contiguous tensor of this type and shape on CUDA device `device`."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != device or device < 0:
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s (got %s %s on %s, strides %s)"
+                         % (name, dtype, tuple(shape), "cuda:%d" % device if device >= 0 else "a CUDA device", t.dtype,
+                            tuple(t.shape), t.device, t.stride()))
 
 
-def _stream(device):
+def _addr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _on(device):
+    """(library, context handle, current stream) of a CUDA device index."""
     import torch
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    ctx = _contexts.get(device)
+    if ctx is None:
+        ctx = context("cuda:%d" % device)
+    return _lib, ctx.handle, torch._C._cuda_getCurrentRawStream(device)
 
 
 def gated_delta_prefill(q, k, v, g, beta, cu_seqlens=None, initial_state=None, output_final_state=False,
@@ -603,7 +612,7 @@ def gated_delta_prefill(q, k, v, g, beta, cu_seqlens=None, initial_state=None, o
         return o.view(v.shape), s
     if q.dim() != 3 or q.shape[-1] != D or v.dim() != 3:
         raise ValueError("q must be [Tt, H, 128] or [B, T, H, 128], got %s" % (tuple(q.shape),))
-    Tt, Hk, H, dev = q.shape[0], q.shape[1], v.shape[1], q.device
+    Tt, Hk, H, dev = q.shape[0], q.shape[1], v.shape[1], q.get_device()
     if Hk < 1 or H < 1 or H % Hk:
         raise ValueError("v has %d heads, not a multiple of the %d q/k heads" % (H, Hk))
     beta16 = beta.dtype == torch.bfloat16
@@ -628,11 +637,11 @@ def gated_delta_prefill(q, k, v, g, beta, cu_seqlens=None, initial_state=None, o
         raise ValueError("cu_seqlens must start at 0, never decrease and end at the %d packed tokens (got %s)"
                          % (Tt, cu_seqlens_host[:8]))
     if plan is None:
-        plan = _cached_plan(cu_seqlens_host, H, _cp_mode(use_intracard_cp), dev.index, plan_gated_delta)
-    elif plan.device != dev.index or plan.shape() != (H, Tt, N) or plan.cu_host != cu_seqlens_host:
+        plan = _cached_plan(cu_seqlens_host, H, _cp_mode(use_intracard_cp), dev, plan_gated_delta)
+    elif plan.device != dev or plan.shape() != (H, Tt, N) or plan.cu_host != cu_seqlens_host:
         raise ValueError("the plan was built for device %s, H=%d, %d tokens, %d sequences (cu_seqlens %s...); the call "
                          "has device %s, H=%d, %d tokens, %d sequences"
-                         % (plan.device, *plan.shape(), plan.cu_host[:4], dev.index, H, Tt, N))
+                         % (plan.device, *plan.shape(), plan.cu_host[:4], dev, H, Tt, N))
     if cu_seqlens is None or isinstance(cu_seqlens, (list, tuple)):
         cu_dev = plan.cu_device()
     else:
@@ -648,20 +657,21 @@ def gated_delta_prefill(q, k, v, g, beta, cu_seqlens=None, initial_state=None, o
     if final_state is not None:
         _need("final_state", final_state, state_dtype, (N, H, D, D), dev)
     elif output_final_state:
-        final_state = torch.empty(N, H, D, D, dtype=state_dtype, device=dev)
+        final_state = torch.empty(N, H, D, D, dtype=state_dtype, device=q.device)
     if out is None:
         out = torch.empty_like(v)
     else:
         _need("out", out, torch.bfloat16, (Tt, H, D), dev)
     n_ws = plan.workspace_bytes()
-    ws = torch.empty(n_ws, dtype=torch.uint8, device=dev) if n_ws else None
+    ws = torch.empty(n_ws, dtype=torch.uint8, device=q.device) if n_ws else None
     if torch.cuda.is_current_stream_capturing() and not any(p is plan for p in _captured_plans):
         _captured_plans.append(plan)
     opts = PrefillOpts(Hk, int(beta16), int(state_dtype == torch.bfloat16))
-    _check(lib().kda_gated_delta_prefill(context(dev).handle, plan.handle, ctypes.byref(opts), _ptr(q), _ptr(k),
-                                         _ptr(v), _ptr(g), _ptr(beta), _ptr(cu_dev), float(scale),
-                                         _ptr(initial_state), _ptr(final_state), _ptr(out), _ptr(ws), n_ws,
-                                         _stream(dev)), "kda_gated_delta_prefill")
+    L, ctx, stream = _on(dev)
+    _check(L.kda_gated_delta_prefill(ctx, plan.handle, ctypes.byref(opts), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                     g.data_ptr(), beta.data_ptr(), cu_dev.data_ptr(), scale, _addr(initial_state),
+                                     _addr(final_state), out.data_ptr(), _addr(ws), n_ws, stream),
+           "kda_gated_delta_prefill")
     return out, final_state
 
 
@@ -679,7 +689,7 @@ def gated_delta_decode(q, k, v, g, beta, state, scale=1.0, out=None, slots=None)
     import torch
     if q.dim() not in (3, 4) or v.dim() != q.dim() or q.shape[-1] != D:
         raise ValueError("q must be [N, H, 128] or [N, T, H, 128] (and v alike), got %s" % (tuple(q.shape),))
-    rows, Hk, H, dev = q.shape[:-2], q.shape[-2], v.shape[-2], q.device
+    rows, Hk, H, dev = q.shape[:-2], q.shape[-2], v.shape[-2], q.get_device()
     N = rows[0]
     if Hk < 1 or H < 1 or H % Hk:
         raise ValueError("v has %d heads, not a multiple of the %d q/k heads" % (H, Hk))
@@ -697,9 +707,10 @@ def gated_delta_decode(q, k, v, g, beta, state, scale=1.0, out=None, slots=None)
         out = torch.empty_like(v)
     else:
         _need("out", out, torch.bfloat16, v.shape, dev)
-    _check(lib().kda_gated_delta_decode(context(dev).handle, N, rows[1] if len(rows) == 2 else 1, H, Hk, D, D,
-                                        _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), float(scale), _ptr(state),
-                                        n_slots, _ptr(slots), _ptr(out), _stream(dev)), "kda_gated_delta_decode")
+    L, ctx, stream = _on(dev)
+    _check(L.kda_gated_delta_decode(ctx, N, rows[1] if len(rows) == 2 else 1, H, Hk, D, D, q.data_ptr(), k.data_ptr(),
+                                    v.data_ptr(), g.data_ptr(), beta.data_ptr(), scale, state.data_ptr(), n_slots,
+                                    _addr(slots), out.data_ptr(), stream), "kda_gated_delta_decode")
     return out
 
 
@@ -733,12 +744,12 @@ def pool_copy(pool, src, dst, page_dim=0):
     pairs with one destination the last counts. In place, returns pool.
     """
     import torch
-    view, dev = _pool(pool, page_dim), pool.device
+    view, dev = _pool(pool, page_dim), pool.get_device()
     n = src.numel()
     _need("src", src, torch.int32, (n,), dev)
     _need("dst", dst, torch.int32, (n,), dev)
-    _check(lib().kda_pool_copy(context(dev).handle, ctypes.byref(view), _ptr(src), _ptr(dst), n, _stream(dev)),
-           "kda_pool_copy")
+    L, ctx, stream = _on(dev)
+    _check(L.kda_pool_copy(ctx, ctypes.byref(view), src.data_ptr(), dst.data_ptr(), n, stream), "kda_pool_copy")
     return pool
 
 
@@ -751,13 +762,14 @@ def pool_fork(pool, used, src, page_dim=0):
     (int32, like src): -1 where the source is no used page or none was free.
     """
     import torch
-    view, dev = _pool(pool, page_dim), pool.device
+    view, dev = _pool(pool, page_dim), pool.get_device()
     n = src.numel()
     _need("src", src, torch.int32, (n,), dev)
     _need("used", used, torch.bool, (view.n_pages,), dev)
     dst = torch.empty_like(src)
-    _check(lib().kda_pool_fork(context(dev).handle, ctypes.byref(view), _ptr(used), _ptr(src), _ptr(dst), n,
-                               _stream(dev)), "kda_pool_fork")
+    L, ctx, stream = _on(dev)
+    _check(L.kda_pool_fork(ctx, ctypes.byref(view), used.data_ptr(), src.data_ptr(), dst.data_ptr(), n, stream),
+           "kda_pool_fork")
     return dst
 
 
@@ -765,11 +777,11 @@ def pool_free(used, pages):
     """Mark pages (int32 CUDA tensor) free in used (bool [n_pages], in place, returned).
     Entries outside the pool are skipped; free and repeated ones are harmless."""
     import torch
-    n, dev = pages.numel(), used.device
+    n, dev = pages.numel(), used.get_device()
     _need("used", used, torch.bool, (used.numel(),), dev)
     _need("pages", pages, torch.int32, (n,), dev)
-    _check(lib().kda_pool_free(context(dev).handle, used.numel(), _ptr(used), _ptr(pages), n, _stream(dev)),
-           "kda_pool_free")
+    L, ctx, stream = _on(dev)
+    _check(L.kda_pool_free(ctx, used.numel(), used.data_ptr(), pages.data_ptr(), n, stream), "kda_pool_free")
     return used
 
 
@@ -783,14 +795,15 @@ def pool_compact(pool, used, table=None, page_dim=0):
     page's new index or -1, and int32 [1], the number of used pages.
     """
     import torch
-    view, dev = _pool(pool, page_dim), pool.device
+    view, dev = _pool(pool, page_dim), pool.get_device()
     _need("used", used, torch.bool, (view.n_pages,), dev)
     if table is not None:
         _need("table", table, torch.int32, table.shape, dev)
-    new_pages = torch.empty(view.n_pages, dtype=torch.int32, device=dev)
-    n_live = torch.empty(1, dtype=torch.int32, device=dev)
-    _check(lib().kda_pool_compact(context(dev).handle, ctypes.byref(view), _ptr(used), _ptr(table),
-                                  0 if table is None else table.numel(), _ptr(new_pages), _ptr(n_live), _stream(dev)),
+    new_pages = torch.empty(view.n_pages, dtype=torch.int32, device=pool.device)
+    n_live = torch.empty(1, dtype=torch.int32, device=pool.device)
+    L, ctx, stream = _on(dev)
+    _check(L.kda_pool_compact(ctx, ctypes.byref(view), used.data_ptr(), _addr(table),
+                              0 if table is None else table.numel(), new_pages.data_ptr(), n_live.data_ptr(), stream),
            "kda_pool_compact")
     return new_pages, n_live
 
@@ -805,14 +818,15 @@ def beam_reorder(pool, slots, parents, page_dim=0):
     states that several beams continue are copied, into pages whose beam ends.
     """
     import torch
-    view, dev = _pool(pool, page_dim), pool.device
+    view, dev = _pool(pool, page_dim), pool.get_device()
     if slots.dim() != 2:
         raise ValueError("slots must be [batch, beams], got %s" % (tuple(slots.shape),))
     _need("slots", slots, torch.int32, slots.shape, dev)
     _need("parents", parents, torch.int32, slots.shape, dev)
     new = torch.empty_like(slots)
-    _check(lib().kda_beam_reorder(context(dev).handle, ctypes.byref(view), _ptr(slots), _ptr(parents), _ptr(new),
-                                  slots.shape[0], slots.shape[1], _stream(dev)), "kda_beam_reorder")
+    L, ctx, stream = _on(dev)
+    _check(L.kda_beam_reorder(ctx, ctypes.byref(view), slots.data_ptr(), parents.data_ptr(), new.data_ptr(),
+                              slots.shape[0], slots.shape[1], stream), "kda_beam_reorder")
     return new
 
 
@@ -830,16 +844,17 @@ def beam_select(logits, scores, n=None, finished=None, eos=None):
     int32, tokens [B, n] int32, finished [B, n] bool, or None without eos).
     """
     import torch
-    if logits.dim() != 3 or logits.device.type != "cuda":
+    dev = logits.get_device()
+    if logits.dim() != 3 or dev < 0:
         raise ValueError("logits must be a CUDA tensor [batch, beams, vocab], got %s on %s"
                          % (tuple(logits.shape), logits.device))
     B, W, V = logits.shape
-    dev = logits.device
     dtype = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}.get(logits.dtype)
     if dtype is None:
         raise ValueError("logits must be fp32, bf16 or fp16, got %s" % logits.dtype)
-    row = logits.stride(1) if W > 1 else logits.stride(0) if B > 1 else V
-    if (V > 1 and logits.stride(2) != 1) or row < V or (B > 1 and logits.stride(0) != W * row):
+    per_entry, per_row, per_token = logits.stride()
+    row = per_row if W > 1 else per_entry if B > 1 else V
+    if (V > 1 and per_token != 1) or row < V or (B > 1 and per_entry != W * row):
         raise ValueError("the rows of logits must be contiguous and evenly spaced (strides %s)" % (logits.stride(),))
     _need("scores", scores, torch.float32, (B, W), dev)
     if finished is not None:
@@ -851,12 +866,13 @@ def beam_select(logits, scores, n=None, finished=None, eos=None):
     n = W if n is None else int(n)
     if not 1 <= n <= 64:
         raise ValueError("n must be in [1, 64], got %d" % n)
-    out_scores = torch.empty(B, n, dtype=torch.float32, device=dev)
-    ids = torch.empty(2, B, n, dtype=torch.int32, device=dev)
-    out_finished = None if eos is None else torch.empty(B, n, dtype=torch.bool, device=dev)
-    n_ws = lib().kda_beam_select_workspace_bytes(B, W, V, n)
-    ws = torch.empty(n_ws, dtype=torch.uint8, device=dev)
-    _check(lib().kda_beam_select(context(dev).handle, B, W, V, n, _ptr(logits), dtype, row, _ptr(scores),
-                                 _ptr(finished), -1 if eos is None else int(eos), _ptr(out_scores), _ptr(ids[0]),
-                                 _ptr(ids[1]), _ptr(out_finished), _ptr(ws), n_ws, _stream(dev)), "kda_beam_select")
-    return out_scores, ids[0], ids[1], out_finished
+    out_scores = torch.empty_like(scores) if n == W else torch.empty(B, n, dtype=torch.float32, device=logits.device)
+    parents, tokens = torch.empty(2, B, n, dtype=torch.int32, device=logits.device).unbind(0)
+    out_finished = None if eos is None else torch.empty(B, n, dtype=torch.bool, device=logits.device)
+    L, ctx, stream = _on(dev)
+    n_ws = L.kda_beam_select_workspace_bytes(B, W, V, n)
+    ws = torch.empty(n_ws, dtype=torch.uint8, device=logits.device)
+    _check(L.kda_beam_select(ctx, B, W, V, n, logits.data_ptr(), dtype, row, scores.data_ptr(), _addr(finished),
+                             -1 if eos is None else int(eos), out_scores.data_ptr(), parents.data_ptr(),
+                             tokens.data_ptr(), _addr(out_finished), ws.data_ptr(), n_ws, stream), "kda_beam_select")
+    return out_scores, parents, tokens, out_finished

@@ -21,7 +21,7 @@ constexpr int32_t kMaxHeads = 1 << 17;  // 32 token rows of one tensor stay belo
 // units of 8 to 2048 chunks: a chunk of a unit with output, one without (a
 // segment's end state or transfer), what a launch of either takes beside its
 // chunks, a merge step and the rest of a merge.
-constexpr double kFullUs = 1.75, kPreUs = 1.55, kUnitUs = 7.0, kMergeUs = 1.6, kMergeLaunchUs = 5.0;
+constexpr double kFullUs = 1.75, kPreUs = 2.3, kUnitUs = 7.0, kMergeUs = 1.0, kMergeLaunchUs = 5.0;
 
 // A launch of units of these chunk counts (longest first), H heads each: one
 // workgroup per compute unit, the next one to whichever is free first.
@@ -59,8 +59,7 @@ double plan_us(const std::vector<int>& nch, int H, int n_cus, int seg) {
         for (int s = 0; s < n; ++s) {
             const int len = (int)((int64_t)c * (s + 1) / n - (int64_t)c * s / n);
             main.push_back(len);
-            if (s + 1 < n)
-                for (int k = 0; k < (s ? 2 : 1); ++k) pre.push_back(len);
+            if (s + 1 < n) pre.push_back(len);
         }
     }
     double us = launch_us(main, H, n_cus, kFullUs);
@@ -130,14 +129,10 @@ kda_status build(int32_t n_cus, const int32_t* cu, int32_t n_seqs, int32_t H, in
             const int c0 = (int)((int64_t)nch[i] * s / n), c1 = (int)((int64_t)nch[i] * (s + 1) / n);
             const int t0 = c0 * kGdChunk, nt = std::min(c1 * kGdChunk, L) - t0;
             p->gd_units.push_back(GdUnit{i, t0, nt, n > 1 ? n_carry + s : GD_INITIAL, s + 1 == n ? GD_FINAL : GD_NONE,
-                                         1});
+                                         GD_NONE});
             if (s + 1 < n) {
-                if (s == 0) {
-                    p->gd_pre.push_back(GdUnit{i, t0, nt, GD_INITIAL, n_sum, 1});
-                } else {
-                    p->gd_pre.push_back(GdUnit{i, t0, nt, GD_ZERO, n_sum + 2 * s - 1, 1});
-                    p->gd_pre.push_back(GdUnit{i, t0, nt, GD_IDENTITY, n_sum + 2 * s, 0});
-                }
+                if (s == 0) p->gd_pre.push_back(GdUnit{i, t0, nt, GD_INITIAL, n_sum, GD_NONE});
+                else p->gd_pre.push_back(GdUnit{i, t0, nt, GD_ZERO, n_sum + 2 * s - 1, n_sum + 2 * s});
             }
             UnitDesc u{};
             u.seq = i;

@@ -350,27 +350,40 @@ __device__ __forceinline__ void chunk_step(const uint8_t* Q, const uint8_t* K, c
     u32x4 kf[4][2];
     const float gc = gs[GS_GAM + 31];
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+    for (int t = 0; t < (OUT ? 4 : 1); ++t)  // without OUT, a tile ahead: 168 registers are there
 #pragma unroll
         for (int s = 0; s < 2; ++s) kf[t][s] = row32(K, t, s);
     if constexpr (OUT) finish_output(rest);
     sched_fence();
     // K S
     Operand sb[4];
-    f32x16 P = zero, below[2];
+    f32x16 P = zero, below;
     u32x4 qf[4][2];
     f32x4 gam[4];
     u32x2 vw[4];
+    auto low = [&](int t, const f32x16& x) __attribute__((always_inline)) {  // lo of S's tile t, then its scaling
+        pack_rows(x, sb[t].l);
 #pragma unroll
-    for (int t = 0; t <= 4; ++t) {
-        if (t < 4) {
-            pack_rows(S[t], sb[t].h);
-            below[t & 1] = rest_of(S[t], sb[t].h, neg);
+        for (int s = 0; s < 2; ++s) P = mfma_32(kf[t][s], sb[t].l[s], P);
+        S[t] = gc * S[t];
+    };
 #pragma unroll
-            for (int s = 0; s < 2; ++s) P = mfma_32(kf[t][s], sb[t].h[s], P);
-        }
-        if constexpr (OUT)
+    for (int t = 0; t < 4; ++t) {
+        pack_rows(S[t], sb[t].h);
+        const f32x16 x = rest_of(S[t], sb[t].h, neg);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) P = mfma_32(kf[t][s], sb[t].h[s], P);
+        if constexpr (OUT) {
             if (t == 1) store(rest.o);
+            if (t > 0) low(t - 1, below);  // a tile behind, so that the matrix unit does not wait
+            below = x;
+        } else {  // the other wavefront of the SIMD fills the wait
+            if (t < 3) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s) kf[t + 1][s] = row32(K, t + 1, s);
+            }
+            low(t, x);
+        }
         if (t == 3) {
 #pragma unroll
             for (int a = 0; a < 4; ++a) {
@@ -379,17 +392,12 @@ __device__ __forceinline__ void chunk_step(const uint8_t* Q, const uint8_t* K, c
                 vw[a] = lds_load_tr16(V + tile_off(8 * a + 4 * h + r, (col0 >> 3) + 2 * (c & 1) + odd) + 8 * (c >> 1));
             }
         }
-        if constexpr (OUT)
-            if (t == 4) {
+        sched_fence();
+    }
+    if constexpr (OUT) {
 #pragma unroll
-                for (int s = 0; s < 4; ++s) qf[s >> 1][s & 1] = row32(Q, s >> 1, s & 1);
-            }
-        if (t > 0) {
-            pack_rows(below[(t - 1) & 1], sb[t - 1].l);
-#pragma unroll
-            for (int s = 0; s < 2; ++s) P = mfma_32(kf[t - 1][s], sb[t - 1].l[s], P);
-            S[t - 1] = gc * S[t - 1];
-        }
+        for (int s = 0; s < 4; ++s) qf[s >> 1][s & 1] = row32(Q, s >> 1, s & 1);
+        low(3, below);
         sched_fence();
     }
     // R = V - diag(gam) K S
@@ -498,10 +506,6 @@ __device__ __forceinline__ void chunk_step(const uint8_t* Q, const uint8_t* K, c
     sched_fence();
 }
 
-__device__ __forceinline__ float load_state(const void* p, int64_t i, bool bf16) {
-    return bf16 ? __uint_as_float((uint32_t)((const uint16_t*)p)[i] << 16) : ((const float*)p)[i];
-}
-
 // Prefill: one workgroup of 8 wavefronts per (unit, head, column tile), in
 // a software pipeline with one barrier per chunk. In interval i
 //   wavefronts 4 .. 7 advance the state over chunk i (16 NT columns each);
@@ -516,7 +520,7 @@ constexpr int DEPTH = 4;  // intervals from a chunk's first load to its use
 template <bool OUT>
 struct Lds {
     alignas(16) uint8_t k[N_QK][TILE_BYTES];
-    alignas(16) uint8_t q[OUT ? N_QK : 1][TILE_BYTES];
+    alignas(16) uint8_t q[OUT ? N_QK : 1][TILE_BYTES];  // without OUT: zeros, the V of a transfer
     alignas(16) uint8_t v[N_V][TILE_BYTES];
     alignas(16) uint8_t t[N_REC][REC4];
     alignas(16) uint8_t a[OUT ? N_REC : 1][REC4];
@@ -555,7 +559,7 @@ struct GdWork {
     uint32_t st_qk, st_v;      // bytes from row to row
     int H, n_tok, n_chunks;
     float scale;
-    bool beta_bf16, with_v;
+    bool beta_bf16;
 };
 
 // The loop of operand wavefront ROLE (a loop per role: values that one role
@@ -578,7 +582,7 @@ __device__ __forceinline__ void produce(const GdWork& w, Lds<OUT>& lds, int lane
     // ring position j is chunk i + j
     for (int i = -DEPTH; i < w.n_chunks; ++i) {
         const int par = i & 1, rows = rows_of_chunk(w.n_tok, i + 4);
-        load(w.v, w.st_v, i + 2, w.with_v ? rows_of_chunk(w.n_tok, i + 2) : 0, lds.v[rv.at[2]]);
+        load(w.v, w.st_v, i + 2, rows_of_chunk(w.n_tok, i + 2), lds.v[rv.at[2]]);
         load(w.k, w.st_qk, i + 4, rows, lds.k[qk.at[4]]);
         if constexpr (OUT) load(w.q, w.st_qk, i + 4, rows, lds.q[qk.at[4]]);
         const bool inside = i + 2 >= 0 && i + 2 < w.n_chunks;
@@ -622,7 +626,10 @@ __device__ __forceinline__ void produce(const GdWork& w, Lds<OUT>& lds, int lane
 }
 
 template <bool OUT>
-__global__ __launch_bounds__(512) void gd_prefill(GdArgs a) {
+constexpr int kThreads = 64 * (4 + (OUT ? 4 : 8));
+
+template <bool OUT>
+__global__ __launch_bounds__(kThreads<OUT>) void gd_prefill(GdArgs a) {
     extern __shared__ __align__(16) uint8_t lds_raw[];
     Lds<OUT>& lds = *(Lds<OUT>*)lds_raw;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -652,7 +659,6 @@ __global__ __launch_bounds__(512) void gd_prefill(GdArgs a) {
         w.n_chunks = n_chunks;
         w.scale = a.scale;
         w.beta_bf16 = a.beta_bf16;
-        w.with_v = un.with_v;
         if (wave == 0) produce<0, OUT>(w, lds, lane);
         else if (wave == 1) produce<1, OUT>(w, lds, lane);
         else if (wave == 2) produce<2, OUT>(w, lds, lane);
@@ -662,11 +668,20 @@ __global__ __launch_bounds__(512) void gd_prefill(GdArgs a) {
 
     // wavefronts 4 .. 7: the state, 32 value columns each. Each shares its SIMD
     // with one operand wavefront and goes first (measured: 247 us without, 232
-    // with, on eight prompts of 512 to 4096 tokens and 32 heads).
+    // with, on eight prompts of 512 to 4096 tokens and 32 heads). Without OUT,
+    // wavefronts 8 .. 11 advance the transfer of the same tokens.
     __builtin_amdgcn_s_setprio(2);
-    const int col0 = 32 * (wave - 4);
+    const int col0 = 32 * (wave & 3);
+    const bool transfer = !OUT && wave >= 8;
+    const int in = transfer ? GD_IDENTITY : un.in, out = transfer ? un.out_m : un.out;
+    if (transfer && out < 0) {
+        for (int i = -DEPTH; i < n_chunks; ++i) lds_barrier();
+        return;
+    }
+    if (transfer)
+        for (int i = (wave & 3) * 64 + lane; i < TILE_BYTES / 16; i += 256) *(u32x4*)(lds.q[0] + 16 * i) = u32x4{0, 0, 0, 0};
     // tile (0, 1) of every operand record
-    for (int i = (wave - 4) * 64 + lane; i < N_REC * 2 * 64; i += 256) {
+    for (int i = (wave & 3) * 64 + lane; !transfer && i < N_REC * 2 * 64; i += 256) {
         const int slot = i >> 7, at = 2048 + (i >> 6 & 1) * 1024 + (32 * (i >> 4 & 1) + (i & 15)) * 16;
         if (!(i >> 5 & 1)) {
             *(u32x4*)(lds.t[slot] + at) = u32x4{0, 0, 0, 0};
@@ -684,10 +699,10 @@ __global__ __launch_bounds__(512) void gd_prefill(GdArgs a) {
                 S[t][i] = f(at0 + (32 * t + 16 * (i >> 3) + (i & 7)) * D, S[t][i]);
     };
     const int64_t own = ((int64_t)un.seq * a.H + h) * (D * D);
-    if (un.in >= 0) {
-        const float* p = a.carries + ((int64_t)un.in * a.H + h) * (D * D);
+    if (in >= 0) {
+        const float* p = a.carries + ((int64_t)in * a.H + h) * (D * D);
         each([&](int at, float) { return p[at]; });
-    } else if (un.in == GD_INITIAL && a.s0) {
+    } else if (in == GD_INITIAL && a.s0) {
         if (a.state_bf16) {
             const uint16_t* p = (const uint16_t*)a.s0 + own;
             each([&](int at, float) { return __uint_as_float((uint32_t)p[at] << 16); });
@@ -696,7 +711,7 @@ __global__ __launch_bounds__(512) void gd_prefill(GdArgs a) {
             each([&](int at, float) { return p[at]; });
         }
     } else {
-        const float one = un.in == GD_IDENTITY ? 1.f : 0.f;
+        const float one = in == GD_IDENTITY ? 1.f : 0.f;
         each([&](int at, float) { return at % (D + 1) == 0 ? one : 0.f; });
     }
     for (int i = -DEPTH; i < 0; ++i) lds_barrier();
@@ -724,7 +739,8 @@ __global__ __launch_bounds__(512) void gd_prefill(GdArgs a) {
         }
     };
     for (int i = 0; i < n_chunks; ++i) {
-        chunk_step<OUT>(lds.q[OUT ? qk.at[0] : 0], lds.k[qk.at[0]], lds.v[rv.at[0]], lds.t[rec.at[0]],
+        chunk_step<OUT>(lds.q[OUT ? qk.at[0] : 0], lds.k[qk.at[0]],
+                        transfer ? lds.q[0] : lds.v[rv.at[0]], lds.t[rec.at[0]],
                         lds.a[OUT ? rec.at[0] : 0], lds.gs[gs.at[0]], a.scale, col0, lane, neg, S, rest,
                         [&](const f32x16& o) __attribute__((always_inline)) { store(i - 1, o); });
         lds_barrier();
@@ -737,10 +753,20 @@ __global__ __launch_bounds__(512) void gd_prefill(GdArgs a) {
         finish_output(rest);
         store(n_chunks - 1, rest.o);
     }
-    if (un.out >= 0) {
-        float* p = a.sums + ((int64_t)un.out * a.H + h) * (D * D);
+    if (transfer) {
+        uint16_t* p = (uint16_t*)(a.sums + ((int64_t)out * a.H + h) * (D * D));
+        each([&](int at, float s) {
+            const int ch = at / D, col = at % D;
+            uint16_t* dst = p + (ch >> 4) * 4096 + (col >> 5) * 1024 + (16 * (col >> 3 & 3) + (ch & 15)) * 8 + (col & 7);
+            const uint32_t hi = pack_bf16(s, 0.f);
+            dst[0] = (uint16_t)hi;
+            dst[512] = (uint16_t)pack_bf16(s - bf16_lo(hi), 0.f);
+            return s;
+        });
+    } else if (out >= 0) {
+        float* p = a.sums + ((int64_t)out * a.H + h) * (D * D);
         each([&](int at, float s) { return p[at] = s; });
-    } else if (un.out == GD_FINAL && a.sT) {
+    } else if (out == GD_FINAL && a.sT) {
         if (a.state_bf16) {
             uint16_t* p = (uint16_t*)a.sT + own;
             each([&](int at, float s) {
@@ -756,13 +782,14 @@ __global__ __launch_bounds__(512) void gd_prefill(GdArgs a) {
 
 // carry_0 = the initial state, carry_1 = the end state of segment 0, then
 // carry_{s+1} = M_s carry_s + B_s. One workgroup of 8 wavefronts per (item,
-// head, 16-column tile); wavefront w forms channels 16w .. 16w + 15, with M and
-// the carry as hi + lo pairs. The carry goes from wavefront to wavefront
-// through LDS, double-buffered, once per segment. The steps are serial, so a
-// step's M and B are loaded while the one before is computed.
-constexpr int CSTR = D + 4;  // floats per column of the carry in LDS
+// head, 16-column tile); wavefront w forms channels 16w .. 16w + 15. M comes as
+// hi + lo pairs; each wavefront splits its part of the carry and passes it on
+// through LDS, double-buffered, once per segment. The steps are serial, so M
+// and B are loaded three steps ahead.
+constexpr int CSTR = D + 8;  // bf16 per column of the carry in LDS
+constexpr int AHEAD = 2;
 __global__ __launch_bounds__(512) void gd_merge(GdMergeArgs a) {
-    __shared__ __align__(16) float carry[2][16 * CSTR];
+    __shared__ __align__(16) uint16_t carry[2][2][16 * CSTR];  // [step parity][hi, lo]
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, gg = lane >> 4, m = lane & 15;
     // the column tiles of a head are n_items * H apart: with a multiple of 8
     // heads they share an XCD, whose L2 then reads M once
@@ -772,58 +799,69 @@ __global__ __launch_bounds__(512) void gd_merge(GdMergeArgs a) {
     const int col = 16 * ct + m, ch = 16 * wave + 4 * gg;
     auto at = [&](int slot) { return ((int64_t)slot * a.H + h) * (D * D) + ch * D + col; };
     struct Step {
-        f32x4 m[4][2], b;
+        u32x4 h[4], l[4];
+        f32x4 b;
     };
-    auto load = [&](Step& x, int s) {  // segment s, or the last transfer there is
+    auto load = [&](Step& x, int s) __attribute__((always_inline)) {  // segment s, or the last transfer there is
         s = s < it.n - 2 ? s : it.n - 2;
-        const float* M = a.sums + ((int64_t)(it.sum0 + 2 * s) * a.H + h) * (D * D) + (16 * wave + m) * D + 8 * gg;
+        const uint8_t* M = (const uint8_t*)(a.sums + ((int64_t)(it.sum0 + 2 * s) * a.H + h) * (D * D)) + wave * 8192 +
+                           lane * 16;
         const float* B = a.sums + at(it.sum0 + 2 * s - 1);
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-            x.m[p][0] = *(const f32x4*)(M + 32 * p);
-            x.m[p][1] = *(const f32x4*)(M + 32 * p + 4);
+            x.h[p] = *(const u32x4*)(M + 2048 * p);
+            x.l[p] = *(const u32x4*)(M + 2048 * p + 1024);
         }
 #pragma unroll
         for (int v = 0; v < 4; ++v) x.b[v] = B[v * D];
     };
-    Step now, next;
-    if (it.n > 2) load(now, 1);
-    f32x4 c;
-    for (int s = 0; s < 2; ++s) {
+    Step x[AHEAD];
+    if (it.n > 2) {
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) load(x[j], 1 + j);
+    }
+    auto put = [&](int s, const f32x4& c) __attribute__((always_inline)) {
         float* dst = a.carries + at(it.carry0 + s);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            c[v] = s ? a.sums[at(it.sum0) + v * D] : a.s0 ? load_state(a.s0, at(it.seq) + v * D, a.state_bf16) : 0.f;
-            dst[v * D] = c[v];
-        }
+        for (int v = 0; v < 4; ++v) dst[v * D] = c[v];
+    };
+    f32x4 c, c0 = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int v = 0; v < 4; ++v) c[v] = a.sums[at(it.sum0) + v * D];
+    if (a.s0 && a.state_bf16) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) c0[v] = __uint_as_float((uint32_t)((const uint16_t*)a.s0)[at(it.seq) + v * D] << 16);
+    } else if (a.s0) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) c0[v] = ((const float*)a.s0)[at(it.seq) + v * D];
     }
-    auto step = [&](Step& x, Step& y, int s) __attribute__((always_inline)) {
-        float* buf = carry[s & 1];
-        *(f32x4*)(buf + m * CSTR + ch) = c;
-        load(y, s + 1);
+    put(0, c0);
+    put(1, c);
+    auto step = [&](Step& x, int s) __attribute__((always_inline)) {
+        uint16_t(*buf)[16 * CSTR] = carry[s & 1];
+        const HiLo own = split4(c);
+        *(u32x2*)(buf[0] + m * CSTR + ch) = own.h;
+        *(u32x2*)(buf[1] + m * CSTR + ch) = own.l;
         lds_barrier();
         c = x.b;
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-            const HiLo a0 = split4(x.m[p][0]), a1 = split4(x.m[p][1]);
-            const float* cc = buf + m * CSTR + 32 * p + 8 * gg;
-            const HiLo b0 = split4(*(const f32x4*)cc), b1 = split4(*(const f32x4*)(cc + 4));
-            const u32x4 ah = {a0.h.x, a0.h.y, a1.h.x, a1.h.y}, al = {a0.l.x, a0.l.y, a1.l.x, a1.l.y};
-            const u32x4 bh = {b0.h.x, b0.h.y, b1.h.x, b1.h.y}, bl = {b0.l.x, b0.l.y, b1.l.x, b1.l.y};
-            c = mfma_k32(al, bh, c);
-            c = mfma_k32(ah, bl, c);
-            c = mfma_k32(ah, bh, c);
+            const u32x4 bh = *(const u32x4*)(buf[0] + m * CSTR + 32 * p + 8 * gg);
+            const u32x4 bl = *(const u32x4*)(buf[1] + m * CSTR + 32 * p + 8 * gg);
+            c = mfma_k32(x.l[p], bh, c);
+            c = mfma_k32(x.h[p], bl, c);
+            c = mfma_k32(x.h[p], bh, c);
         }
-        float* dst = a.carries + at(it.carry0 + s + 1);
-#pragma unroll
-        for (int v = 0; v < 4; ++v) dst[v * D] = c[v];
+        load(x, s + AHEAD);
+        put(s + 1, c);
     };
     int s = 1;
-    for (; s + 2 < it.n; s += 2) {
-        step(now, next, s);
-        step(next, now, s + 1);
-    }
-    if (s + 1 < it.n) step(now, next, s);
+    for (; s + AHEAD < it.n; s += AHEAD)
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) step(x[j], s + j);
+#pragma unroll
+    for (int j = 0; j + 1 < AHEAD; ++j)
+        if (s + j + 1 < it.n) step(x[j], s + j);
 }
 
 // Decode. With S the state before a token and gam = exp(g), for value column j:
@@ -929,7 +967,7 @@ hipError_t run_gd_prefill(const GdArgs& a, hipStream_t s) {
             if (dev < 256) done[dev >> 6] |= 1ull << (dev & 63);
         }
     }
-    const dim3 grid((unsigned)(a.n_units * a.H)), block(512);
+    const dim3 grid((unsigned)(a.n_units * a.H)), block(kThreads<OUT>);
     hipLaunchKernelGGL((gd_prefill<OUT>), grid, block, sizeof(Lds<OUT>), s, a);
     return hipGetLastError();
 }

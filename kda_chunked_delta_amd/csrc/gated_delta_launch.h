@@ -17,7 +17,7 @@ struct GdUnit {
     int32_t n_tok;  // tokens to run (may be 0)
     int32_t in;     // GD_ZERO, GD_INITIAL, GD_IDENTITY, or a carry slot (>= 0)
     int32_t out;    // GD_NONE, GD_FINAL, or a summary slot (>= 0)
-    int32_t with_v; // 0: V := 0 (a segment's transfer)
+    int32_t out_m;  // where the transfer of the tokens goes: GD_NONE or a summary slot
 };
 enum : int32_t { GD_ZERO = -1, GD_INITIAL = -2, GD_IDENTITY = -3 };
 enum : int32_t { GD_NONE = -1, GD_FINAL = -2 };
