@@ -18,10 +18,11 @@ namespace {
 constexpr int32_t kMaxHeads = 1 << 17;  // 32 token rows of one tensor stay below 2^31 bytes
 
 // Cost model of a plan, microseconds on MI355X, fitted to launches of 8 to 2048
-// units of 8 to 2048 chunks: a chunk of a unit with output, one without (a
-// segment's end state or transfer), what a launch of either takes beside its
-// chunks, a merge step and the rest of a merge.
-constexpr double kFullUs = 1.75, kPreUs = 2.3, kUnitUs = 7.0, kMergeUs = 1.0, kMergeLaunchUs = 5.0;
+// units of 8 to 2048 chunks: a chunk of a unit with output, one of a segment's
+// end state and transfer, what a launch of either takes beside its chunks, a
+// merge step and the rest of a merge. Chunks take kBusy more while every compute
+// unit is at work: matrix instructions at that rate lower the clock.
+constexpr double kFullUs = 1.7, kPreUs = 2.25, kBusy = 0.28, kUnitUs = 7.0, kMergeUs = 1.0, kMergeLaunchUs = 5.0;
 
 // A launch of units of these chunk counts (longest first), H heads each: one
 // workgroup per compute unit, the next one to whichever is free first.
@@ -31,7 +32,7 @@ double launch_us(std::vector<int> chunks, int H, int n_cus, double per_chunk) {
     const int64_t n = (int64_t)chunks.size() * H;
     double total = 0;
     for (int c : chunks) total += (double)c * H;
-    if (n > 16384) return kUnitUs + per_chunk * std::max((double)chunks[0], total / n_cus + chunks[0]);
+    if (n > 16384) return kUnitUs + per_chunk * (1 + kBusy) * (total / n_cus + chunks[0]);
     std::priority_queue<double, std::vector<double>, std::greater<double>> busy;
     double end = 0;
     for (int c : chunks)
@@ -45,17 +46,18 @@ double launch_us(std::vector<int> chunks, int H, int n_cus, double per_chunk) {
             busy.push(t);
             end = std::max(end, t);
         }
-    return end;
+    return end * (1 + kBusy * per_chunk * total / (end * n_cus));
 }
 
 int segments_of(int chunks, int seg) { return seg > 0 && chunks > seg ? (chunks + seg - 1) / seg : 1; }
 
 double plan_us(const std::vector<int>& nch, int H, int n_cus, int seg) {
     std::vector<int> main, pre;
-    int most = 1;
+    int most = 1, items = 0;
     for (int c : nch) {
         const int n = segments_of(c, seg);
         most = std::max(most, n);
+        items += n > 1;
         for (int s = 0; s < n; ++s) {
             const int len = (int)((int64_t)c * (s + 1) / n - (int64_t)c * s / n);
             main.push_back(len);
@@ -63,7 +65,10 @@ double plan_us(const std::vector<int>& nch, int H, int n_cus, int seg) {
         }
     }
     double us = launch_us(main, H, n_cus, kFullUs);
-    if (most > 1) us += launch_us(pre, H, n_cus, kPreUs) + (most - 2) * kMergeUs + kMergeLaunchUs;
+    if (most > 1) {
+        const double rounds = std::max(1.0, 8.0 * items * H / n_cus);  // 8 workgroups per item and head
+        us += launch_us(pre, H, n_cus, kPreUs) + (most - 2) * rounds * kMergeUs + kMergeLaunchUs;
+    }
     return us;
 }
 
@@ -112,7 +117,8 @@ kda_status build(int32_t n_cus, const int32_t* cu, int32_t n_seqs, int32_t H, in
                     seg = c;
                 }
             }
-            if (mode == KDA_CP_AUTO && t_serial <= t_cp) seg = 0;
+            // segments do more work for a shorter chain: cut only for what the model is sure of
+            if (mode == KDA_CP_AUTO && 0.93 * t_serial <= t_cp) seg = 0;
         }
     }
     kda_plan* p = new kda_plan();
