@@ -669,8 +669,9 @@ def gated_delta_prefill(q, k, v, g, beta, cu_seqlens=None, initial_state=None, o
     opts = PrefillOpts(Hk, int(beta16), int(state_dtype == torch.bfloat16))
     L, ctx, stream = _on(dev)
     _check(L.kda_gated_delta_prefill(ctx, plan.handle, ctypes.byref(opts), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                     g.data_ptr(), beta.data_ptr(), cu_dev.data_ptr(), scale, _addr(initial_state),
-                                     _addr(final_state), out.data_ptr(), _addr(ws), n_ws, stream),
+                                     g.data_ptr(), beta.data_ptr(), cu_dev.data_ptr(), float(scale),
+                                     _addr(initial_state), _addr(final_state), out.data_ptr(), _addr(ws), n_ws,
+                                     stream),
            "kda_gated_delta_prefill")
     return out, final_state
 
@@ -709,8 +710,8 @@ def gated_delta_decode(q, k, v, g, beta, state, scale=1.0, out=None, slots=None)
         _need("out", out, torch.bfloat16, v.shape, dev)
     L, ctx, stream = _on(dev)
     _check(L.kda_gated_delta_decode(ctx, N, rows[1] if len(rows) == 2 else 1, H, Hk, D, D, q.data_ptr(), k.data_ptr(),
-                                    v.data_ptr(), g.data_ptr(), beta.data_ptr(), scale, state.data_ptr(), n_slots,
-                                    _addr(slots), out.data_ptr(), stream), "kda_gated_delta_decode")
+                                    v.data_ptr(), g.data_ptr(), beta.data_ptr(), float(scale), state.data_ptr(),
+                                    n_slots, _addr(slots), out.data_ptr(), stream), "kda_gated_delta_decode")
     return out
 
 

@@ -9,7 +9,7 @@
 // exp(x - maximum), and its n first (logit, token) keys, which are also its
 // first by value. beam_pick joins the chunks: the log-sum-exp of each row and
 // every value in fp64 (candidates of two beams can lie closer than fp32
-// resolves), then n times the best head of the sorted lists.
+// resolves), then the n best entries of the sorted lists.
 #include "kda.h"
 #include "state_pool_launch.h"
 
@@ -129,8 +129,10 @@ __device__ __forceinline__ uint64_t nth_key(uint32_t value, uint32_t token, int 
 // keys, and only n groups have keys at or above it: those (at most 4 n N, in
 // practice little more than n) are ranked by counting.
 //
-// Measured on 32 x 8 rows of 131072 bf16 logits, n = 16 (67 MB): 71 us with
-// the edge from ranks over all 256 threads' first keys, which took most of it.
+// Measured on 32 x 8 rows of 131072 bf16 logits, n = 16 (67 MB): 26 us, 2.6 TB/s,
+// half of it the stream and half the edge and the exponentials (71 us with the
+// edge from ranks over all 256 threads' first keys). Every load of a thread is
+// in flight at once.
 template <int DT, int VECS>
 __global__ __launch_bounds__(256) void beam_rows(BeamArgs a) {
     constexpr int PER = 16 / Elem<DT>::SIZE, N = VECS * PER;
@@ -154,7 +156,8 @@ __global__ __launch_bounds__(256) void beam_rows(BeamArgs a) {
             x[i] = load16<DT>(base + (int64_t)t0 * Elem<DT>::SIZE);
         } else {
 #pragma unroll
-            for (int j = 0; j < PER; ++j) Elem<DT>::set(x[i], j, t0 + j < a.vocab ? Elem<DT>::raw(base, t0 + j) : Elem<DT>::NONE);
+            for (int j = 0; j < PER; ++j)
+                Elem<DT>::set(x[i], j, t0 + j < a.vocab ? Elem<DT>::raw(base, t0 + j) : Elem<DT>::NONE);
         }
     }
     if (tid == 0) s_count = 0;
@@ -268,7 +271,14 @@ constexpr int ROW_PLAIN = 0, ROW_EMPTY = 1, ROW_FINISHED = 2;
 
 // Keys of a batch entry that are staged in LDS, and lists that a lane then keeps
 // the heads of in registers; larger entries are read from memory.
-constexpr int PICK_LDS_KEYS = 6144, PICK_LANE_LISTS = 4;
+constexpr int PICK_LDS_KEYS = 5632, PICK_LANE_LISTS = 4;
+constexpr int PICK_RANKED = 512;  // candidates that are ranked by counting
+
+// Unsigned order of a candidate's value; 0 is no candidate.
+__device__ __forceinline__ uint64_t order_of(const Cand& c) {
+    const uint64_t bits = __builtin_bit_cast(uint64_t, c.v);
+    return c.beam == NO_BEAM ? 0 : bits ^ (bits >> 63 ? ~0ull : 1ull << 63);
+}
 
 // The larger of two unsigned numbers over the wavefront, by DPP.
 __device__ __forceinline__ uint32_t wave_umax(uint32_t x) {
@@ -284,39 +294,58 @@ __device__ __forceinline__ uint32_t wave_umax(uint32_t x) {
 
 // One workgroup per batch entry. A row is `splits` sorted lists, or one list
 // made up on the spot: a finished beam's end token and then -inf, or -inf
-// throughout (no logit or score above -inf). All wavefronts stage the keys;
-// then the first selects: each lane keeps the heads of its lists, a round takes
-// the best of them (by the upper half of the value's bits, which is nearly
-// always enough), and its owner moves on. Bound by the latency of n such rounds
-// (measured: 1.1 us each with the heads looked up anew, n = 16, 128 lists).
+// throughout (no logit or score above -inf). All wavefronts stage the keys. The
+// n-th best of 64 groups of lists' heads (by the upper half of the value's bits)
+// is a lower edge of the n best; the candidates at or above it, little more
+// than n, are ranked by counting. Where more than PICK_RANKED tie, and
+// where the keys do not fit LDS, the first wavefront takes n rounds: each lane
+// keeps the heads of its lists, the best of them goes out and its owner moves
+// on. Bound by latency: 32 entries of 8 beams and 128 lists with n = 16 take
+// 12 us, of which the launch is 3; by rounds it was 21.
 template <bool STAGED>
 __global__ __launch_bounds__(256) void beam_pick(BeamArgs a) {
     __shared__ double s_log[kBeamMax];
     __shared__ float s_top[kBeamMax], s_score[kBeamMax];
     __shared__ int s_kind[kBeamMax];
     __shared__ uint64_t s_keys[STAGED ? PICK_LDS_KEYS : 1];
+    __shared__ uint64_t s_order[STAGED ? PICK_RANKED : 1], s_key[STAGED ? PICK_RANKED : 1];
+    __shared__ uint32_t s_beam[STAGED ? PICK_RANKED : 1], s_first[STAGED ? 64 * PICK_LANE_LISTS : 1], s_edge;
+    __shared__ int s_count;
     extern __shared__ uint16_t s_pos[];  // [beams * splits] entries taken of each list
     const int tid = threadIdx.x, lane = tid & 63;
     const int64_t row0 = (int64_t)blockIdx.x * a.beams;
     const int lists = a.beams * a.splits;
     const uint64_t* keys = a.keys + row0 * a.splits * a.n;
-    if constexpr (STAGED)
-        for (int i = tid; i < lists * a.n; i += 256) s_keys[i] = keys[i];
-    // maximum and sum of the rows: 4 lanes per row
-    {
-        const int w = tid >> 2, sub = tid & 3;
+    if constexpr (STAGED) {
+        const int total = lists * a.n;
+        for (int base = tid; base < total; base += 8 * 256) {  // eight loads in flight
+            uint64_t k[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) k[j] = keys[base + 256 * j < total ? base + 256 * j : base];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (base + 256 * j < total) s_keys[base + 256 * j] = k[j];
+        }
+    }
+    // maximum and sum of the rows: 16 lanes per row
+    for (int w0 = 0; w0 < a.beams; w0 += 16) {
+        const int w = w0 + (tid >> 4), sub = tid & 15;
         const bool row = w < a.beams && !(a.finished && a.finished[row0 + w]);
         const float* mx = a.maxima + (row0 + w) * a.splits;
         const double* sm = a.sums + (row0 + w) * a.splits;
-        float top = NEG_INF;
+        const float m0 = row && sub < a.splits ? mx[sub] : NEG_INF;
+        const double s0 = row && sub < a.splits ? sm[sub] : 0;
+        float top = m0;
         if (row)
-            for (int i = sub; i < a.splits; i += 4) top = mx[i] > top ? mx[i] : top;
-        for (int d = 1; d < 4; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
-        double sum = 0;
+            for (int i = sub + 16; i < a.splits; i += 16) top = mx[i] > top ? mx[i] : top;
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+        auto part = [&](float m, double s) { return m == top ? s : s * exp((double)m - (double)top); };
+        double sum = part(m0, s0);
         if (row)
-            for (int i = sub; i < a.splits; i += 4)
-                sum += mx[i] == top ? sm[i] : sm[i] * exp((double)mx[i] - (double)top);
-        for (int d = 1; d < 4; d <<= 1) sum += __shfl_xor(sum, d, 64);
+            for (int i = sub + 16; i < a.splits; i += 16) sum += part(mx[i], sm[i]);
+#pragma unroll
+        for (int d = 1; d < 16; d <<= 1) sum += __shfl_xor(sum, d, 64);
         if (w < a.beams && sub == 0) {
             const float sc = clean(a.scores[row0 + w]);
             s_kind[w] = !row ? ROW_FINISHED : top == NEG_INF || sc == NEG_INF ? ROW_EMPTY : ROW_PLAIN;
@@ -327,8 +356,8 @@ __global__ __launch_bounds__(256) void beam_pick(BeamArgs a) {
     }
     if constexpr (!STAGED)
         for (int l = tid; l < lists; l += 256) s_pos[l] = 0;
+    if (tid == 0) s_count = 0;
     __syncthreads();
-    if (tid >= 64) return;
     const double none = -__builtin_huge_val();
     // entry `pos` of list l, which belongs to beam w: its key (0: none) and value
     auto entry = [&](int l, int w, int pos, bool first_list) __attribute__((always_inline)) {
@@ -351,6 +380,14 @@ __global__ __launch_bounds__(256) void beam_pick(BeamArgs a) {
         }
         if (c.key) c.beam = (uint32_t)w;
         return c;
+    };
+    auto emit = [&](int i, double v, uint32_t beam, uint64_t key) __attribute__((always_inline)) {
+        const int64_t o = (int64_t)blockIdx.x * a.n + i;
+        const int32_t token = (int32_t)~(uint32_t)key;
+        a.out_scores[o] = (float)v;
+        a.out_parents[o] = (int32_t)beam;
+        a.out_tokens[o] = token;
+        if (a.out_finished) a.out_finished[o] = token == a.eos || s_kind[beam] == ROW_FINISHED;
     };
     Cand best;
     int from;
@@ -378,6 +415,58 @@ __global__ __launch_bounds__(256) void beam_pick(BeamArgs a) {
         }
     };
     if constexpr (STAGED) {
+        const int l = tid < lists ? tid : 0, w = l / a.splits;  // a list per thread
+        Cand c{none, NO_BEAM, 0};
+        if (tid < lists) c = entry(l, w, 0, l == w * a.splits);
+        uint64_t order = order_of(c);
+        s_first[tid] = (uint32_t)(order >> 32);
+        __syncthreads();
+        if (tid < 64) {
+            uint32_t first = 0, v = 0;
+#pragma unroll
+            for (int q = 0; q < PICK_LANE_LISTS; ++q) {
+                const uint32_t x = s_first[lane + 64 * q];
+                first = x > first ? x : first;
+            }
+#pragma unroll
+            for (int b = 31; b >= 0; --b) {
+                const uint32_t x = v | 1u << b;
+                v = __popcll(__ballot(first >= x)) >= a.n ? x : v;
+            }
+            if (tid == 0) s_edge = v;
+        }
+        __syncthreads();
+        const uint32_t edge = s_edge;
+        for (int i = 0; order != 0 && (uint32_t)(order >> 32) >= edge;) {
+            const int at = atomicAdd(&s_count, 1);
+            if (at < PICK_RANKED) {
+                s_order[at] = order;
+                s_beam[at] = c.beam;
+                s_key[at] = c.key;
+            }
+            if (++i == a.n) break;
+            c = entry(l, w, i, l == w * a.splits);
+            order = order_of(c);
+        }
+        __syncthreads();
+        const int count = s_count;
+        if (count <= PICK_RANKED) {
+            for (int i = tid; i < count; i += 256) {
+                const uint64_t order = s_order[i], key = s_key[i];
+                const uint32_t beam = s_beam[i];
+                int rank = 0;
+                for (int j = 0; j < count; ++j) {
+                    const uint64_t o = s_order[j];
+                    rank += o > order || (o == order && (s_beam[j] < beam || (s_beam[j] == beam && s_key[j] > key)));
+                }
+                const uint64_t bits = order >> 63 ? order ^ 1ull << 63 : ~order;
+                if (rank < a.n) emit(rank, __builtin_bit_cast(double, bits), beam, key);
+            }
+            return;
+        }
+    }
+    if (tid >= 64) return;
+    if constexpr (STAGED) {
 #pragma unroll
         for (int q = 0; q < PICK_LANE_LISTS; ++q) {
             const int l = lane + 64 * q;
@@ -388,8 +477,7 @@ __global__ __launch_bounds__(256) void beam_pick(BeamArgs a) {
     }
     choose();
     for (int i = 0; i < a.n; ++i) {
-        const uint64_t bits = __builtin_bit_cast(uint64_t, best.v);
-        const uint64_t order = best.beam == NO_BEAM ? 0 : bits ^ (bits >> 63 ? ~0ull : 1ull << 63);
+        const uint64_t order = order_of(best);
         const uint32_t hi = wave_umax((uint32_t)(order >> 32));
         uint64_t at = __ballot((uint32_t)(order >> 32) == hi);
         if (at & (at - 1)) {  // the rest of the value, then beam and key
@@ -403,12 +491,7 @@ __global__ __launch_bounds__(256) void beam_pick(BeamArgs a) {
             at = __ballot((at >> lane & 1) && (uint32_t)best.key == k0);
         }
         if (at >> lane & 1 && best.beam != NO_BEAM) {
-            const int64_t o = (int64_t)blockIdx.x * a.n + i;
-            const int32_t token = (int32_t)~(uint32_t)best.key;
-            a.out_scores[o] = (float)best.v;
-            a.out_parents[o] = (int32_t)best.beam;
-            a.out_tokens[o] = token;
-            if (a.out_finished) a.out_finished[o] = token == a.eos || s_kind[best.beam] == ROW_FINISHED;
+            emit(i, best.v, best.beam, best.key);
             if constexpr (STAGED) {
 #pragma unroll
                 for (int q = 0; q < PICK_LANE_LISTS; ++q)

@@ -290,20 +290,11 @@ __device__ __forceinline__ int opaque(int x) {
     return x;
 }
 
-// Scheduling: nothing moves across sched_fence, and interleave<M, V>(n) asks
-// for n groups of M matrix and V vector instructions.
+// Nothing is scheduled across sched_fence.
 __device__ __forceinline__ void sched_fence() { __builtin_amdgcn_sched_barrier(0); }
 // Fixes the place of what forms or uses x among the other pins.
 template <class T>
 __device__ __forceinline__ void pin(T& x) { asm volatile("" : "+v"(x)); }
-template <int N, int M, int V>
-__device__ __forceinline__ void interleave() {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x8, M, 0);
-        __builtin_amdgcn_sched_group_barrier(0x2, V, 0);
-    }
-}
 // What is left of a chunk's output when its state is done: o (scaled by gam)
 // and the operands of A U.
 struct Rest {
@@ -506,14 +497,24 @@ __device__ __forceinline__ void chunk_step(const uint8_t* Q, const uint8_t* K, c
     sched_fence();
 }
 
-// Prefill: one workgroup of 8 wavefronts per (unit, head, column tile), in
-// a software pipeline with one barrier per chunk. In interval i
-//   wavefronts 4 .. 7 advance the state over chunk i (16 NT columns each);
+// Prefill: one workgroup per (unit, head), in a software pipeline with one
+// barrier per chunk. In interval i
+//   wavefronts 4 .. 7 advance the state over chunk i (32 columns each); without
+//     OUT, wavefronts 8 .. 11 do the same for the transfer M of the unit's
+//     tokens, the end state from the identity with V = 0, on the same operands;
 //   wavefronts 0 .. 3 form the operands of later chunks: 0, 1 and 2 the tiles
 //     of (I + L)^-1 of chunk i + 2 and 3 its A, wavefront 2 also T10 of chunk
 //     i + 1 (from the tiles published by the last barrier) and the row values
 //     of chunk i + 3, and all four issue the loads of q, k (chunk i + 4) and v
 //     (chunk i + 2), which must have landed by the end of interval i + 1.
+// Bound by the chain of chunks when there are few units (1.7 us a chunk, 2.2
+// without OUT), and by the matrix units when every compute unit is at work:
+// at 2.2 and 2.9 us a chunk they do 1.06 PFLOP/s, where a large matrix product
+// reaches 1.41 on this card, and the clock falls from 2.4 to 2.1 GHz. Measured:
+// 65536 tokens of 8 heads, 196 us without OUT (two launch-wide passes over 31
+// segments when B and M had a workgroup each: 230) and 157 with; eight prompts
+// of 512 to 4096 tokens and 32 heads, 240 us (first kernel, on 16x16x32 products
+// and without the pipeline: 544).
 // Ring slots: q and k 5 chunks, v and the operands 3, the row values 4.
 constexpr int N_QK = 5, N_V = 3, N_REC = 3, N_GS = 4;
 constexpr int DEPTH = 4;  // intervals from a chunk's first load to its use
@@ -679,7 +680,8 @@ __global__ __launch_bounds__(kThreads<OUT>) void gd_prefill(GdArgs a) {
         return;
     }
     if (transfer)
-        for (int i = (wave & 3) * 64 + lane; i < TILE_BYTES / 16; i += 256) *(u32x4*)(lds.q[0] + 16 * i) = u32x4{0, 0, 0, 0};
+        for (int i = (wave & 3) * 64 + lane; i < TILE_BYTES / 16; i += 256)
+            *(u32x4*)(lds.q[0] + 16 * i) = u32x4{0, 0, 0, 0};
     // tile (0, 1) of every operand record
     for (int i = (wave & 3) * 64 + lane; !transfer && i < N_REC * 2 * 64; i += 256) {
         const int slot = i >> 7, at = 2048 + (i >> 6 & 1) * 1024 + (32 * (i >> 4 & 1) + (i & 15)) * 16;
@@ -753,11 +755,12 @@ __global__ __launch_bounds__(kThreads<OUT>) void gd_prefill(GdArgs a) {
         finish_output(rest);
         store(n_chunks - 1, rest.o);
     }
-    if (transfer) {
+    if (transfer) {  // hi and lo in gd_merge's order: [channel / 16][column / 32][hi, lo][lane][8]
         uint16_t* p = (uint16_t*)(a.sums + ((int64_t)out * a.H + h) * (D * D));
         each([&](int at, float s) {
             const int ch = at / D, col = at % D;
-            uint16_t* dst = p + (ch >> 4) * 4096 + (col >> 5) * 1024 + (16 * (col >> 3 & 3) + (ch & 15)) * 8 + (col & 7);
+            const int to = 16 * (col >> 3 & 3) + (ch & 15);
+            uint16_t* dst = p + (ch >> 4) * 4096 + (col >> 5) * 1024 + to * 8 + (col & 7);
             const uint32_t hi = pack_bf16(s, 0.f);
             dst[0] = (uint16_t)hi;
             dst[512] = (uint16_t)pack_bf16(s - bf16_lo(hi), 0.f);
@@ -783,9 +786,12 @@ __global__ __launch_bounds__(kThreads<OUT>) void gd_prefill(GdArgs a) {
 // carry_0 = the initial state, carry_1 = the end state of segment 0, then
 // carry_{s+1} = M_s carry_s + B_s. One workgroup of 8 wavefronts per (item,
 // head, 16-column tile); wavefront w forms channels 16w .. 16w + 15. M comes as
-// hi + lo pairs; each wavefront splits its part of the carry and passes it on
-// through LDS, double-buffered, once per segment. The steps are serial, so M
-// and B are loaded three steps ahead.
+// hi + lo pairs in the order of the operands; each wavefront splits its part of
+// the carry and passes it on through LDS, double-buffered, once per segment.
+// The steps are serial, so M and B are loaded two steps ahead. Bound by what
+// one compute unit loads, 72 KiB a step: 30 steps take 32 us, and took 56 with
+// M as rows, whose 64-byte pieces a load instruction fetches at half the rate
+// (splitting M here or three steps ahead made no difference to either).
 constexpr int CSTR = D + 8;  // bf16 per column of the carry in LDS
 constexpr int AHEAD = 2;
 __global__ __launch_bounds__(512) void gd_merge(GdMergeArgs a) {
@@ -830,7 +836,8 @@ __global__ __launch_bounds__(512) void gd_merge(GdMergeArgs a) {
     for (int v = 0; v < 4; ++v) c[v] = a.sums[at(it.sum0) + v * D];
     if (a.s0 && a.state_bf16) {
 #pragma unroll
-        for (int v = 0; v < 4; ++v) c0[v] = __uint_as_float((uint32_t)((const uint16_t*)a.s0)[at(it.seq) + v * D] << 16);
+        for (int v = 0; v < 4; ++v)
+            c0[v] = __uint_as_float((uint32_t)((const uint16_t*)a.s0)[at(it.seq) + v * D] << 16);
     } else if (a.s0) {
 #pragma unroll
         for (int v = 0; v < 4; ++v) c0[v] = ((const float*)a.s0)[at(it.seq) + v * D];
@@ -872,7 +879,12 @@ __global__ __launch_bounds__(512) void gd_merge(GdMergeArgs a) {
 // owns rows 16rs .. + 15 of columns 4cg .. + 3, so a load instruction covers
 // eight whole 128-byte lines, the sums need three lane exchanges and the
 // kernel needs neither LDS nor a barrier. Bound by HBM: 128 KiB of state
-// traffic per (sequence, head) against 1 KiB per token.
+// traffic per (sequence, head) against 1 KiB per token; 256 sequences of 32
+// heads take 193 us (5.6 TB/s). One sequence takes 7 us, which is the latency
+// of the launch and of one load after another.
+//
+// States beyond 128 MiB, half the last-level cache, are read and written with
+// the nontemporal hint: they cannot stay cached until the next step anyway.
 constexpr int DEC_W = 4;  // wavefronts (32-column tiles) per workgroup
 
 template <bool NT>

@@ -126,6 +126,16 @@ def test_ties_go_to_the_lowest_index(V):
     check(y.expand(3, 4, V).contiguous(), torch.full((3, 4), -2.0, device=DEV), n=12)
 
 
+@pytest.mark.parametrize("W,V,n", [(8, 20000, 16), (4, 9000, 7), (3, 50000, 33)])
+def test_more_ties_than_are_ranked_at_once(W, V, n):
+    """Equal logits and scores: every candidate ties with every other."""
+    say("case all tie", W, V, n)
+    x = torch.full((2, W, V), 0.5, device=DEV)
+    s = torch.full((2, W), -3.0, device=DEV)
+    x[1, :, 100:] = -1.0  # a hundred per beam, in the first chunk
+    check(x, s, n=n)
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("pad,shift", [(0, 1), (3, 0), (5, 3)])
 def test_strided_rows(dtype, pad, shift):
