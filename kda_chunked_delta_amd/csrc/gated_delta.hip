@@ -507,14 +507,13 @@ __device__ __forceinline__ void chunk_step(const uint8_t* Q, const uint8_t* K, c
 //     i + 1 (from the tiles published by the last barrier) and the row values
 //     of chunk i + 3, and all four issue the loads of q, k (chunk i + 4) and v
 //     (chunk i + 2), which must have landed by the end of interval i + 1.
-// Bound by the chain of chunks when there are few units (1.7 us a chunk, 2.2
-// without OUT), and by the matrix units when every compute unit is at work:
-// at 2.2 and 2.9 us a chunk they do 1.06 PFLOP/s, where a large matrix product
-// reaches 1.41 on this card, and the clock falls from 2.4 to 2.1 GHz. Measured:
-// 65536 tokens of 8 heads, 196 us without OUT (two launch-wide passes over 31
-// segments when B and M had a workgroup each: 230) and 157 with; eight prompts
-// of 512 to 4096 tokens and 32 heads, 240 us (first kernel, on 16x16x32 products
-// and without the pipeline: 544).
+// Bound by the chain of chunks: 1.7 us each with few units (2.25 without OUT),
+// 2.2 (2.9) when every compute unit is at work and the clock falls from 2.4 to
+// 2.0 GHz. The matrix units are then busy for 45% of the cycles, vector instructions
+// issue for a third; products and splits of one chunk wait for each other. Measured: 65536 tokens of 8 heads, 200 us without OUT (230 with a
+// workgroup each for B and M) and 157 with; eight prompts of 512 to 4096 tokens
+// and 32 heads, 240 us (first kernel, on 16x16x32 products and without the
+// pipeline: 544).
 // Ring slots: q and k 5 chunks, v and the operands 3, the row values 4.
 constexpr int N_QK = 5, N_V = 3, N_REC = 3, N_GS = 4;
 constexpr int DEPTH = 4;  // intervals from a chunk's first load to its use
