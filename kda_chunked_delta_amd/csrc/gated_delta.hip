@@ -36,7 +36,8 @@ __device__ __forceinline__ int tile_off(int row, int gi) { return row * 256 + ((
 
 // Rows 4i .. 4i + 3 of a tile by one direct-to-LDS load. Rows past the
 // descriptor's range become zeros.
-__device__ __forceinline__ void load_rows(__amdgpu_buffer_rsrc_t rsrc, uint32_t stride, int i, int lane, uint8_t* tile) {
+__device__ __forceinline__ void load_rows(__amdgpu_buffer_rsrc_t rsrc, uint32_t stride, int i, int lane,
+                                          uint8_t* tile) {
     const int row = 4 * i + (lane >> 4);
     const uint32_t off = (uint32_t)row * stride + (((lane & 15) ^ gd_swz(row)) << 4);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)(tile + 1024 * i), 16,
@@ -509,8 +510,9 @@ __device__ __forceinline__ void chunk_step(const uint8_t* Q, const uint8_t* K, c
 //     (chunk i + 2), which must have landed by the end of interval i + 1.
 // Bound by the chain of chunks: 1.7 us each with few units (2.25 without OUT),
 // 2.2 (2.9) when every compute unit is at work and the clock falls from 2.4 to
-// 2.0 GHz. The matrix units are then busy for 45% of the cycles, vector instructions
-// issue for a third; products and splits of one chunk wait for each other. Measured: 65536 tokens of 8 heads, 200 us without OUT (230 with a
+// 2.0 GHz. The matrix units are then busy for 45% of the cycles, vector
+// instructions issue for a third; products and splits of one chunk wait for
+// each other. Measured: 65536 tokens of 8 heads, 200 us without OUT (230 with a
 // workgroup each for B and M) and 157 with; eight prompts of 512 to 4096 tokens
 // and 32 heads, 240 us (first kernel, on 16x16x32 products and without the
 // pipeline: 544).
@@ -571,7 +573,8 @@ __device__ __forceinline__ void produce(const GdWork& w, Lds<OUT>& lds, int lane
     Ring<N_REC> rec;
     Ring<N_GS> gs;
     // a chunk's rows by the four wavefronts, 8 each
-    auto load = [&](const uint8_t* base, uint32_t stride, int c, int rows, uint8_t* tile) __attribute__((always_inline)) {
+    auto load = [&](const uint8_t* base, uint32_t stride, int c, int rows, uint8_t* tile)
+                    __attribute__((always_inline)) {
         const auto rsrc = chunk_rsrc(base + (size_t)(c < 0 ? 0 : c) * GC * stride, (uint32_t)rows * stride);
         load_rows(rsrc, stride, 2 * ROLE, lane, tile);
         load_rows(rsrc, stride, 2 * ROLE + 1, lane, tile);
@@ -731,7 +734,8 @@ __global__ __launch_bounds__(kThreads<OUT>) void gd_prefill(GdArgs a) {
     Rest rest = {};
     // the output rows of chunk i (none before the first)
     auto store = [&](int i, const f32x16& o) __attribute__((always_inline)) {
-        const auto rsrc = chunk_rsrc(ob + (size_t)(i < 0 ? 0 : i) * GC * st_v, (uint32_t)rows_of_chunk(n_tok, i) * st_v);
+        const uint32_t bytes = (uint32_t)rows_of_chunk(n_tok, i) * st_v;
+        const auto rsrc = chunk_rsrc(ob + (size_t)(i < 0 ? 0 : i) * GC * st_v, bytes);
         const int at = (int)((lane & 31) * st_v) + (col0 + 16 * (lane >> 5)) * 2;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {

@@ -256,3 +256,19 @@ def test_beam_search_over_the_state_pool():
         got = f(pool[slots.long()])
         live = torch.isfinite(best)
         assert (got - states)[live].norm() <= 1e-5 * states[live].norm()
+
+
+def test_logits_beyond_2_31_elements():
+    """The last batch entries of 4.4 GB of logits select what they select alone."""
+    B, W, V = 33, 8, 8200000
+    say("case logits beyond 2^31 elements")
+    x = torch.empty(B, W, V, dtype=torch.bfloat16, device=DEV)
+    x.normal_(generator=torch.Generator(device=DEV).manual_seed(3))
+    x[:, :, 1234567] = torch.arange(20, 20 + W, device=DEV).to(torch.bfloat16)  # each beam's first, all apart
+    s = torch.linspace(-1.0, 0.0, B * W, device=DEV).view(B, W)
+    got = kda.beam_select(x, s, n=W)
+    alone = kda.beam_select(x[-2:].contiguous(), s[-2:], n=W)
+    for a, b in zip(got[1:3], alone[1:3]):
+        assert torch.equal(a[-2:], b)
+    # two log-sum-exps, each within 2e-7, and two roundings
+    assert ((got[0][-2:] - alone[0]).abs() <= 4e-7 + 2.0 ** -23 * alone[0].abs()).all()

@@ -322,3 +322,51 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for i, (o, s) in enumerate(got):
         assert torch.equal(o, want[i % 2][0]) and torch.equal(s, want[i % 2][1])
+
+
+# ---------------------------------------------------------------------------
+# offsets beyond 32 bits
+# ---------------------------------------------------------------------------
+def test_decode_of_a_slot_beyond_4_gib():
+    """A pool of 8.4 GiB: the slots behind 2^31 elements give the bits of a small pool."""
+    H, P = 32, 4200
+    say("case decode, slots beyond 2^31 elements")
+    d = decode_case(3, 2, H, H, seed=71)
+    args = [d[x] for x in ("q", "k", "v", "g", "beta")]
+    pool = torch.zeros(P, H, D, D, device=DEV)
+    slots = torch.tensor([P - 1, 4097, 2049], dtype=torch.int32, device=DEV)
+    pool[slots.long()] = d["initial_state"]
+    state = d["initial_state"].clone()
+    o = kda.gated_delta_decode(*args, pool, slots=slots)
+    want = kda.gated_delta_decode(*args, state)
+    assert torch.equal(o, want) and torch.equal(pool[slots.long()], state)
+    pool[slots.long()] = 0.0
+    assert torch.count_nonzero(pool) == 0
+
+
+def test_prefill_tokens_beyond_4_gib():
+    """262250 tokens of 64 heads (4.3 GB of v): the prompts behind the long one give
+    the bits of a batch of their own. Segmented outputs are off the unsegmented
+    ones by a rounding each, half a bf16 step (2^-8 of the value), and the
+    states' tolerance."""
+    H, Hk, lengths = 64, 1, [262000, 100, 33, 117]
+    say("case prefill beyond 4 GiB")
+    cu = [sum(lengths[:i]) for i in range(len(lengths) + 1)]
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    q, k = (torch.nn.functional.normalize(torch.randn(cu[-1], Hk, D, generator=gen, device=DEV), dim=-1).bfloat16()
+            for _ in range(2))
+    v = torch.empty(cu[-1], H, D, dtype=torch.bfloat16, device=DEV).normal_(generator=gen)
+    g = -0.2 * torch.rand(cu[-1], H, generator=gen, device=DEV)
+    beta = torch.rand(cu[-1], H, generator=gen, device=DEV)
+    tail = [x[cu[1]:].contiguous() for x in (q, k, v, g, beta)]
+    want, sw = kda.gated_delta_prefill(*tail, cu_seqlens=[c - cu[1] for c in cu[1:]], output_final_state=True,
+                                       use_intracard_cp=False)
+    for cp in (False, True):
+        o, s = kda.gated_delta_prefill(q, k, v, g, beta, cu_seqlens=cu, output_final_state=True,
+                                       plan=kda.plan_gated_delta(cu, H, cp, 512 if cp else 0, device=DEV))
+        assert torch.equal(o[cu[1]:], want) and torch.equal(s[1:], sw)
+        if not cp:
+            first, s_first = o[:cu[1]], s[:1]
+        else:
+            close("state", s[:1], s_first.double(), 2 * STATE_TOL)
+            assert (o[:cu[1]].float() - first.float()).abs().max() <= (2 * HALF + 2 * STATE_TOL) * first.float().abs().max()
