@@ -505,14 +505,14 @@ __device__ __forceinline__ void chunk_step(const uint8_t* Q, const uint8_t* K, c
 //     tokens, the end state from the identity with V = 0, on the same operands;
 //   wavefronts 0 .. 3 form the operands of later chunks: 0, 1 and 2 the tiles
 //     of (I + L)^-1 of chunk i + 2 and 3 its A, wavefront 2 also T10 of chunk
-//     i + 1 (from the tiles published by the last barrier) and the row values
-//     of chunk i + 3, and all four issue the loads of q, k (chunk i + 4) and v
+//     i + 1 (from the tiles published by the last barrier), 2 or (without OUT)
+//     3 the row values of chunk i + 3, and all four issue the loads of q, k (chunk i + 4) and v
 //     (chunk i + 2), which must have landed by the end of interval i + 1.
 // Bound by the chain of chunks: 1.7 us each with few units (2.25 without OUT),
 // 2.2 (2.9) when every compute unit is at work and the clock falls from 2.4 to
 // 2.0 GHz. The matrix units are then busy for 45% of the cycles, vector
 // instructions issue for a third; products and splits of one chunk wait for
-// each other. Measured: 65536 tokens of 8 heads, 200 us without OUT (230 with a
+// each other. Measured: 65536 tokens of 8 heads, 190 us without OUT (230 with a
 // workgroup each for B and M) and 157 with; eight prompts of 512 to 4096 tokens
 // and 32 heads, 240 us (first kernel, on 16x16x32 products and without the
 // pipeline: 544).
@@ -579,7 +579,8 @@ __device__ __forceinline__ void produce(const GdWork& w, Lds<OUT>& lds, int lane
         load_rows(rsrc, stride, 2 * ROLE, lane, tile);
         load_rows(rsrc, stride, 2 * ROLE + 1, lane, tile);
     };
-    float x = 0.f;  // ROLE 2: log-decay of row lane & 31, and its beta's bits
+    constexpr int SCAN = OUT ? 2 : 3;  // who forms the row values: the A of OUT takes wavefront 3 longer
+    float x = 0.f;  // SCAN: log-decay of row lane & 31, and its beta's bits
     uint32_t b = 0;
     f32x4 l10 = {0.f, 0.f, 0.f, 0.f};
     // ring position j is chunk i + j
@@ -595,13 +596,14 @@ __device__ __forceinline__ void produce(const GdWork& w, Lds<OUT>& lds, int lane
             if (inside) diag_tile<0>(K, g, lds.lt, lds.t00[par], lds.t[rec.at[2]], lane);
         } else if constexpr (ROLE == 1) {
             if (inside) diag_tile<1>(K, g, lds.lt + LMAT, lds.t11[par], lds.t[rec.at[2]], lane);
-        } else if constexpr (ROLE == 3) {
-            if constexpr (OUT)
-                if (inside) qk_tiles(lds.q[qk.at[2]], K, g, w.scale, lds.a[rec.at[2]], lane);
-        } else {
+        } else if constexpr (ROLE == 3 && OUT) {
+            if (inside) qk_tiles(lds.q[qk.at[2]], K, g, w.scale, lds.a[rec.at[2]], lane);
+        } else if constexpr (ROLE == 2) {
             if (i + 1 >= 0 && i + 1 < w.n_chunks)
                 off_diagonal(l10, lds.t00[par ^ 1], lds.t11[par ^ 1], lds.gs[gs.at[1]], lds.t[rec.at[1]], lane);
             if (inside) l10 = lower_tile(K, g, lane);
+        }
+        if constexpr (ROLE == SCAN) {
             row_scan(x, w.beta_bf16 ? __uint_as_float(b << 16) : __uint_as_float(b), lane, lds.gs[gs.at[3]]);
             const uint32_t at = (uint32_t)(lane & 31) * (uint32_t)w.H, n = rows ? (uint32_t)(rows - 1) * w.H + 1 : 0u;
             const size_t c = (size_t)(i + 4) * GC * w.H;
@@ -614,8 +616,8 @@ __device__ __forceinline__ void produce(const GdWork& w, Lds<OUT>& lds, int lane
                 b = __builtin_amdgcn_raw_buffer_load_b32(chunk_rsrc((const float*)w.beta + c, n * 4), (int)(at * 4), 0,
                                                          0);
         }
-        // the loads of the last interval have landed (role 2 has waited for its own, to scan them)
-        if constexpr (ROLE != 2) {
+        // the loads of the last interval have landed (SCAN has waited for its own, to scan them)
+        if constexpr (ROLE != SCAN) {
             if constexpr (OUT) asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
             else asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
         }
