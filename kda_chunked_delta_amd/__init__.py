@@ -593,8 +593,9 @@ def gated_delta_prefill(q, k, v, g, beta, cu_seqlens=None, initial_state=None, o
     cu_seqlens, the states, scale, out and the returned (o, final_state or
     None) are as in prefill. use_intracard_cp: "auto" cuts long sequences with
     few heads into segments (equal up to fp32-level rounding), False never
-    does. plan: from plan_gated_delta. The workspace of a segmented plan comes
-    from torch's allocator, on the current stream.
+    does. plan: from plan_gated_delta; made on the first call with these
+    cu_seqlens otherwise, which a graph capture cannot. The workspace of a
+    segmented plan comes from torch's allocator, on the current stream.
     """
     import torch
     if q.dim() == 4:
@@ -621,11 +622,14 @@ def gated_delta_prefill(q, k, v, g, beta, cu_seqlens=None, initial_state=None, o
     _need("v", v, torch.bfloat16, (Tt, H, D), dev)
     _need("g", g, torch.float32, (Tt, H), dev)
     _need("beta", beta, torch.bfloat16 if beta16 else torch.float32, (Tt, H), dev)
+    capturing = torch.cuda.is_current_stream_capturing()
     if cu_seqlens_host is None:
         if cu_seqlens is None:
             cu_seqlens_host = [0, Tt]
         elif isinstance(cu_seqlens, (list, tuple)):
             cu_seqlens_host = cu_seqlens
+        elif capturing:
+            raise ValueError("a graph capture needs cu_seqlens_host: device cu_seqlens cannot be read in it")
         else:
             cu_seqlens_host = cu_seqlens.tolist()  # host copy for the planner (synchronises)
     cu_seqlens_host = [int(x) for x in cu_seqlens_host]
@@ -637,12 +641,19 @@ def gated_delta_prefill(q, k, v, g, beta, cu_seqlens=None, initial_state=None, o
         raise ValueError("cu_seqlens must start at 0, never decrease and end at the %d packed tokens (got %s)"
                          % (Tt, cu_seqlens_host[:8]))
     if plan is None:
-        plan = _cached_plan(cu_seqlens_host, H, _cp_mode(use_intracard_cp), dev, plan_gated_delta)
+        mode = _cp_mode(use_intracard_cp)
+        if capturing and (dev, tuple(cu_seqlens_host), H, mode, plan_gated_delta) not in _plan_cache:
+            raise ValueError("a graph capture needs a plan made before it: pass plan=plan_gated_delta(...), or call "
+                             "once with these cu_seqlens")
+        plan = _cached_plan(cu_seqlens_host, H, mode, dev, plan_gated_delta)
     elif plan.device != dev or plan.shape() != (H, Tt, N) or plan.cu_host != cu_seqlens_host:
         raise ValueError("the plan was built for device %s, H=%d, %d tokens, %d sequences (cu_seqlens %s...); the call "
                          "has device %s, H=%d, %d tokens, %d sequences"
                          % (plan.device, *plan.shape(), plan.cu_host[:4], dev, H, Tt, N))
     if cu_seqlens is None or isinstance(cu_seqlens, (list, tuple)):
+        if capturing and plan._cu_dev is None:
+            raise ValueError("a graph capture needs cu_seqlens on the device: pass them as a tensor, or call "
+                             "plan.cu_device() before it")
         cu_dev = plan.cu_device()
     else:
         cu_dev = cu_seqlens
@@ -664,7 +675,7 @@ def gated_delta_prefill(q, k, v, g, beta, cu_seqlens=None, initial_state=None, o
         _need("out", out, torch.bfloat16, (Tt, H, D), dev)
     n_ws = plan.workspace_bytes()
     ws = torch.empty(n_ws, dtype=torch.uint8, device=q.device) if n_ws else None
-    if torch.cuda.is_current_stream_capturing() and not any(p is plan for p in _captured_plans):
+    if capturing and not any(p is plan for p in _captured_plans):
         _captured_plans.append(plan)
     opts = PrefillOpts(Hk, int(beta16), int(state_dtype == torch.bfloat16))
     L, ctx, stream = _on(dev)

@@ -306,6 +306,26 @@ def test_graph_replay_on_another_stream(seg):
         assert torch.equal(o, want[0]) and torch.equal(o1, want[1]) and torch.equal(state, eager)
 
 
+def test_capture_refuses_what_would_break_it():
+    """Without a plan, with device cu_seqlens alone, or with a table that is not on the device yet."""
+    d = make([70, 41], 2, seed=77)
+    xs = [d[x] for x in ("q", "k", "v", "g", "beta")]
+    plan = kda.plan_gated_delta([0, 70, 111], 2, device=DEV)
+    cu = torch.tensor([0, 70, 111], dtype=torch.int32, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for kw in (dict(cu_seqlens=[0, 70, 111]), dict(cu_seqlens=cu), dict(cu_seqlens=[0, 70, 111], plan=plan)):
+            with pytest.raises(ValueError, match="capture"):
+                kda.gated_delta_prefill(*xs, **kw)
+        o, _ = kda.gated_delta_prefill(*xs, cu_seqlens=cu, cu_seqlens_host=[0, 70, 111], plan=plan)
+    want, _ = kda.gated_delta_prefill(*xs, cu_seqlens=cu)
+    for _ in range(3):
+        o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want)
+
+
 def test_two_streams_at_once():
     ds = [make([600], 2, seed=s, g_mul=0.05) for s in (1, 2)]
     plan = kda.plan_gated_delta([0, 600], 2, True, 4, device=DEV)
