@@ -295,13 +295,14 @@ __device__ __forceinline__ uint32_t wave_umax(uint32_t x) {
 // One workgroup per batch entry. A row is `splits` sorted lists, or one list
 // made up on the spot: a finished beam's end token and then -inf, or -inf
 // throughout (no logit or score above -inf). All wavefronts stage the keys. The
-// n-th best of 64 groups of lists' heads (by the upper half of the value's bits)
-// is a lower edge of the n best; the candidates at or above it, little more
-// than n, are ranked by counting. Where more than PICK_RANKED tie, and
+// n-th best of 256 entries, the first of every list (by the upper bits of the
+// value), is a lower edge of the n best; the candidates at or above it, little
+// more than n, are ranked by counting. Where more than PICK_RANKED tie, and
 // where the keys do not fit LDS, the first wavefront takes n rounds: each lane
 // keeps the heads of its lists, the best of them goes out and its owner moves
 // on. Bound by latency: 32 entries of 8 beams and 128 lists with n = 16 take
-// 12 us, of which the launch is 3; by rounds it was 21.
+// 11 us, of which 3 are the launch (23 with the rounds on lists in memory); 32
+// lists with n = 16 as many (16 by rounds).
 template <bool STAGED>
 __global__ __launch_bounds__(256) void beam_pick(BeamArgs a) {
     __shared__ double s_log[kBeamMax];
@@ -415,36 +416,39 @@ __global__ __launch_bounds__(256) void beam_pick(BeamArgs a) {
         }
     };
     if constexpr (STAGED) {
-        const int l = tid < lists ? tid : 0, w = l / a.splits;  // a list per thread
+        // the threads share the lists evenly, each every `step`-th entry of one
+        const int shift = lists > 1 ? 32 - __builtin_clz(lists - 1) : 0, step = 256 >> shift;
+        const int l = tid >> (8 - shift), w = l / a.splits;
+        int i = tid & (step - 1);
         Cand c{none, NO_BEAM, 0};
-        if (tid < lists) c = entry(l, w, 0, l == w * a.splits);
+        if (l < lists && i < a.n) c = entry(l, w, i, l == w * a.splits);
         uint64_t order = order_of(c);
         s_first[tid] = (uint32_t)(order >> 32);
         __syncthreads();
         if (tid < 64) {
-            uint32_t first = 0, v = 0;
+            uint32_t x[4], v = 0;
 #pragma unroll
-            for (int q = 0; q < PICK_LANE_LISTS; ++q) {
-                const uint32_t x = s_first[lane + 64 * q];
-                first = x > first ? x : first;
-            }
+            for (int q = 0; q < 4; ++q) x[q] = s_first[lane + 64 * q];
 #pragma unroll
-            for (int b = 31; b >= 0; --b) {
-                const uint32_t x = v | 1u << b;
-                v = __popcll(__ballot(first >= x)) >= a.n ? x : v;
+            for (int b = 31; b >= 12; --b) {  // 8 bits of a double's mantissa are enough
+                const uint32_t e = v | 1u << b;
+                int count = 0;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) count += __popcll(__ballot(x[q] >= e));
+                v = count >= a.n ? e : v;
             }
             if (tid == 0) s_edge = v;
         }
         __syncthreads();
         const uint32_t edge = s_edge;
-        for (int i = 0; order != 0 && (uint32_t)(order >> 32) >= edge;) {
+        while (order != 0 && (uint32_t)(order >> 32) >= edge) {
             const int at = atomicAdd(&s_count, 1);
             if (at < PICK_RANKED) {
                 s_order[at] = order;
                 s_beam[at] = c.beam;
                 s_key[at] = c.key;
             }
-            if (++i == a.n) break;
+            if ((i += step) >= a.n) break;
             c = entry(l, w, i, l == w * a.splits);
             order = order_of(c);
         }
