@@ -8,9 +8,8 @@ namespace kda {
 
 constexpr int kGdChunk = 32;  // tokens per chunk of the gated delta prefill
 
-// A run of tokens of one sequence, advanced by one workgroup per (head, column
-// tile). `in` and `out` name the state it starts from and where its end state
-// goes.
+// A run of tokens of one sequence, advanced by one workgroup per head. `in` and
+// `out` name the state it starts from and where its end state goes.
 struct GdUnit {
     int32_t seq;
     int32_t tok0;   // first token within the sequence
@@ -25,7 +24,7 @@ enum : int32_t { GD_NONE = -1, GD_FINAL = -2 };
 // The segments 0 .. n - 1 of one sequence. Carry slot carry0 + s holds the
 // state before segment s; summary slot sum0 the end state of segment 0, slots
 // sum0 + 2 s - 1 and sum0 + 2 s the end state B_s from zero and the transfer
-// M_s of segment s = 1 .. n - 2.
+// M_s of segment s = 1 .. n - 2 (M as pairs of bf16 in the merge's own order).
 struct GdMerge {
     int32_t seq;
     int32_t n;
