@@ -18,7 +18,13 @@ namespace {
 
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LOG2E_LO = (float)(1.4426950408889634 - (double)LOG2E);
-constexpr float LN2 = 0.6931471805599453f;
+constexpr double LN2 = 0.6931471805599453;
+// Up to this maximum a chunk's exponentials are taken as they are: e^48 and its
+// sums are far inside fp32, and what flushes to zero (logits below -87) is below
+// e^-39 of the maximum's term. Beyond it, with |x - m| < 32, x and m are both
+// multiples of 2^-19 (|x| > 16, |m| > 32), and so is their difference, which
+// 24 bits hold; terms further off are below e^-32 of the maximum's.
+constexpr float REF_MAX = 48.f;
 constexpr float NEG_INF = -__builtin_huge_valf();
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -120,9 +126,13 @@ __device__ __forceinline__ uint64_t nth_key(uint32_t value, uint32_t token, int 
 //
 // Sums. A chunk's elements and the order of its sums depend on the row's
 // length alone, not on its address: equal rows get equal sums, and their
-// candidates tie. exp(x - m) is exp2 of (x - m) log2(e) with the product's
-// rounding put back in, added in pairs and then in fp64, which leaves exp2's
-// own last bit (2^-23) and one rounding (2^-24) at most.
+// candidates tie. Terms are exp(x - r) with r = 0 where the maximum m allows it,
+// so that no bit of x is lost (x - m in fp32 is off by 2^-21 from |x - m| = 8 on,
+// the same way for equal logits), and r = m beyond REF_MAX, where x - m is exact
+// as long as the term counts. exp(d) is exp2 of d log2(e); that product's rounding
+// is put back in by a sum of its own, sum(exp2 * rounding). The exponentials are
+// added in pairs and then in fp64, which leaves exp2's own last bit (2^-23) and
+// one rounding (2^-24) at most.
 //
 // Keys. The 256 threads form 64 groups of 4 (one lane of each wavefront). The
 // n-th largest of the groups' first keys is a lower edge of the chunk's n first
@@ -139,7 +149,7 @@ __global__ __launch_bounds__(256) void beam_rows(BeamArgs a) {
     extern __shared__ uint64_t s_cand[];  // [4 n N]
     __shared__ uint32_t s_value[4][64], s_token[4][64];
     __shared__ float s_max[4];
-    __shared__ double s_sum[4];
+    __shared__ double s_sum[4], s_scale;
     __shared__ uint64_t s_edge;
     __shared__ int s_count;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -194,6 +204,11 @@ __global__ __launch_bounds__(256) void beam_rows(BeamArgs a) {
         if (lane == 0) s_edge = edge;
     }
     const float m = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
+    const float ref = __builtin_fabsf(m) <= REF_MAX ? 0.f : m;
+    if (wave == 1) {  // the sum is handed on relative to the maximum; the first wavefront forms the edge meanwhile
+        const double f = ref == m ? 1.0 : exp(-(double)m);
+        if (lane == 0) s_scale = f;
+    }
     double sum = 0.0;
     if (__builtin_isinf(m)) {  // no logit above -inf: all count as 1; or some at +inf, which share the row
 #pragma unroll
@@ -202,6 +217,7 @@ __global__ __launch_bounds__(256) void beam_rows(BeamArgs a) {
             for (int j = 0; j < PER; ++j)
                 if (first + i * 256 * PER + j < a.vocab && Elem<DT>::get(x[i], j) == m) sum += 1.0;
     } else {
+        float rest = 0.f;  // sum of exp2(hi) * lo
 #pragma unroll
         for (int i = 0; i < VECS; ++i)
 #pragma unroll
@@ -210,14 +226,15 @@ __global__ __launch_bounds__(256) void beam_rows(BeamArgs a) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     // -inf and NaN become -200, whose exponential is 0
-                    const float d = fmaxf(Elem<DT>::get(x[i], j + u) - m, -200.f);
+                    const float d = fmaxf(Elem<DT>::get(x[i], j + u) - ref, -200.f);
                     const float hi = d * LOG2E;
                     const float lo = __builtin_fmaf(d, LOG2E_LO, __builtin_fmaf(d, LOG2E, -hi));
-                    const float p = __builtin_amdgcn_exp2f(hi);
-                    e[u] = __builtin_fmaf(p, lo * LN2, p);
+                    e[u] = __builtin_amdgcn_exp2f(hi);
+                    rest = __builtin_fmaf(e[u], lo, rest);
                 }
                 sum += (double)(e[0] + e[1]);
             }
+        sum += (double)rest * LN2;
     }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d, 64);
@@ -249,7 +266,7 @@ __global__ __launch_bounds__(256) void beam_rows(BeamArgs a) {
     for (int i = count + tid; i < a.n; i += 256) out[i] = 0;
     if (tid == 0) {
         a.maxima[row * a.splits + split] = m;
-        a.sums[row * a.splits + split] = s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3];
+        a.sums[row * a.splits + split] = (s_sum[0] + s_sum[1] + s_sum[2] + s_sum[3]) * s_scale;
     }
 }
 
