@@ -616,11 +616,9 @@ __device__ __forceinline__ void produce(const GdWork& w, Lds<OUT>& lds, int lane
                 b = __builtin_amdgcn_raw_buffer_load_b32(chunk_rsrc((const float*)w.beta + c, n * 4), (int)(at * 4), 0,
                                                          0);
         }
-        // the loads of the last interval have landed (SCAN has waited for its own, to scan them)
-        if constexpr (ROLE != SCAN) {
-            if constexpr (OUT) asm volatile("s_waitcnt vmcnt(6)" ::: "memory");
-            else asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
-        }
+        // the loads of the last interval have landed: at most this one's (q, k, v; g and beta) are still on their way
+        constexpr int ISSUED = (OUT ? 6 : 4) + (ROLE == SCAN ? 2 : 0);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(ISSUED) : "memory");
         lds_barrier();
         qk.next();
         rv.next();
