@@ -435,8 +435,9 @@ kda_status kda_debug_k1_records(kda_ctx *ctx, const kda_plan *plan, const void *
  * transfer matrix are formed first, the states between segments merged from
  * them, and all segments then run side by side; the results differ from the
  * unsegmented ones by fp32-level rounding. Errors and the upload of the
- * tables are as in kda_plan_prefill; H is at most 131072. The plan is only
- * accepted by kda_gated_delta_prefill, and the inspection calls. */
+ * tables are as in kda_plan_prefill; H is at most 131072, and H times the
+ * sequences and segments below 2^23 (what one launch takes; forced segments a
+ * little less). The plan is only accepted by kda_gated_delta_prefill, and the inspection calls. */
 kda_status kda_plan_gated_delta(kda_ctx *ctx, const int32_t *cu_seqlens_host, int32_t n_seqs, int32_t H,
                                 int32_t dk, int32_t dv, kda_cp_mode mode, int32_t seg_chunks, kda_plan **out);
 
@@ -476,8 +477,8 @@ kda_status kda_gated_delta_prefill_validate(const kda_plan *plan, const kda_pref
  *   state   : fp32 [n_slots, H, 128, 128]; slots (device int32 [n_seqs], or
  *             NULL with n_slots = n_seqs) as in kda_decode_slots: a slot
  *             outside the pool skips its sequence, and no two may be equal
- * Alignment, aliasing and errors as in kda_decode_slots. One launch, no
- * workspace. */
+ * n_seqs * H is below 2^24. Alignment, aliasing and errors as in
+ * kda_decode_slots. One launch, no workspace. */
 kda_status kda_gated_delta_decode(kda_ctx *ctx, int32_t n_seqs, int32_t n_tokens, int32_t H, int32_t qk_heads,
                                   int32_t dk, int32_t dv, const void *q, const void *k, const void *v, const float *g,
                                   const float *beta, float scale, float *state, int32_t n_slots, const int32_t *slots,
@@ -546,7 +547,7 @@ kda_status kda_pool_compact_validate(const kda_pool *pool, const uint8_t *used, 
  * beam that continues a parent keeps its page, the others take, in order, the
  * pages of the parents that no beam continues. A beam whose parent is outside
  * [0, beams) gets one of the pages left over, with undefined contents. new_slots may
- * not overlap slots or parents. */
+ * not overlap slots or parents. batch * beams pages are fewer than 2^24 parts of 16 KiB. */
 kda_status kda_beam_reorder(kda_ctx *ctx, const kda_pool *pool, const int32_t *slots, const int32_t *parents,
                             int32_t *new_slots, int32_t batch, int32_t beams, hipStream_t stream);
 kda_status kda_beam_reorder_validate(const kda_pool *pool, const int32_t *slots, const int32_t *parents,
@@ -571,7 +572,9 @@ typedef enum { KDA_FP32 = 0, KDA_BF16 = 1, KDA_FP16 = 2 } kda_dtype;
  * NaN logits and scores count as -inf; a row without a logit above -inf has
  * all candidates at -inf; +inf logits share their row's probability. Values
  * are compared in fp64, with the log-sum-exp within 2e-7 (equal rows tie exactly). beams <= 64,
- * n <= 64 and n <= beams * vocab. The workspace (16-byte aligned, of
+ * n <= 64 and n <= beams * vocab. A row is taken in chunks of 2048 logits (8192 for
+ * large batches with n <= 32): at most 24576 chunks per batch entry, and fewer than
+ * 2^24 in all. The workspace (16-byte aligned, of
  * kda_beam_select_workspace_bytes) is the caller's until the call's work is
  * done; calls that may run at the same time need one each. */
 size_t kda_beam_select_workspace_bytes(int32_t batch, int32_t beams, int32_t vocab, int32_t n);

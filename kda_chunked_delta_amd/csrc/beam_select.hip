@@ -144,7 +144,7 @@ __device__ __forceinline__ uint64_t nth_key(uint32_t value, uint32_t token, int 
 // edge from ranks over all 256 threads' first keys). Every load of a thread is
 // in flight at once.
 template <int DT, int VECS>
-__global__ __launch_bounds__(256) void beam_rows(BeamArgs a) {
+__global__ __launch_bounds__(kBeamThreads) void beam_rows(BeamArgs a) {
     constexpr int PER = 16 / Elem<DT>::SIZE, N = VECS * PER;
     extern __shared__ uint64_t s_cand[];  // [4 n N]
     __shared__ uint32_t s_value[4][64], s_token[4][64];
@@ -321,7 +321,7 @@ __device__ __forceinline__ uint32_t wave_umax(uint32_t x) {
 // 11 us, of which 3 are the launch (23 with the rounds on lists in memory); 32
 // lists with n = 16 as many (16 by rounds).
 template <bool STAGED>
-__global__ __launch_bounds__(256) void beam_pick(BeamArgs a) {
+__global__ __launch_bounds__(kBeamThreads) void beam_pick(BeamArgs a) {
     __shared__ double s_log[kBeamMax];
     __shared__ float s_top[kBeamMax], s_score[kBeamMax];
     __shared__ int s_kind[kBeamMax];
@@ -530,7 +530,7 @@ __global__ __launch_bounds__(256) void beam_pick(BeamArgs a) {
 
 template <int DT>
 hipError_t rows(const BeamArgs& a, hipStream_t s) {
-    const dim3 grid((unsigned)((int64_t)a.batch * a.beams * a.splits)), block(256);
+    const dim3 grid((unsigned)((int64_t)a.batch * a.beams * a.splits)), block(kBeamThreads);
     constexpr int PER = 16 / Elem<DT>::SIZE;
     const int vecs = a.chunk / (256 * PER);
     const size_t lds = (size_t)4 * a.n * vecs * PER * sizeof(uint64_t);
@@ -548,7 +548,7 @@ hipError_t launch_beam_rows(const BeamArgs& a, int dtype, hipStream_t s) {
 }
 
 hipError_t launch_beam_pick(const BeamArgs& a, hipStream_t s) {
-    const dim3 grid((unsigned)a.batch), block(256);
+    const dim3 grid((unsigned)a.batch), block(kBeamThreads);
     const int64_t lists = (int64_t)a.beams * a.splits;
     if (lists * a.n <= PICK_LDS_KEYS && lists <= 64 * PICK_LANE_LISTS)
         hipLaunchKernelGGL(beam_pick<true>, grid, block, 0, s, a);

@@ -159,10 +159,12 @@ kda_status build(int32_t n_cus, const int32_t* cu, int32_t n_seqs, int32_t H, in
     std::stable_sort(p->gd_pre.begin(), p->gd_pre.end(), longer);
     std::stable_sort(p->units.begin(), p->units.end(),
                      [](const UnitDesc& a, const UnitDesc& b) { return a.n_chunks > b.n_chunks; });
-    if ((int64_t)std::max(p->gd_units.size(), p->gd_pre.size()) * H > INT32_MAX / 16) {
+    if (!launchable((int64_t)p->gd_units.size() * H, kGdThreads) ||
+        !launchable((int64_t)p->gd_pre.size() * H, kGdSegmentThreads) ||
+        !launchable((int64_t)p->gd_merges.size() * H * kGdMergeTiles, kGdMergeThreads)) {
+        const size_t n_units = p->gd_units.size();
         delete p;
-        return fail(KDA_ERR_INVALID, "kda_plan_gated_delta: too many work units (%zu units, %d heads)",
-                    p->gd_units.size(), H);
+        return fail(KDA_ERR_INVALID, "kda_plan_gated_delta: too many work units (%zu units, %d heads)", n_units, H);
     }
     p->off_b = 0;
     p->off_carry = (size_t)n_sum * H * kStateBytes;
@@ -377,7 +379,7 @@ kda_status kda_gated_delta_decode_validate(int32_t n_seqs, int32_t n_tokens, int
     if (!slots && n_slots != n_seqs)
         return fail(KDA_ERR_INVALID, "%s: without a slot table the state holds n_seqs = %d states, not %d", who,
                     n_seqs, n_slots);
-    if ((int64_t)n_seqs * H > INT32_MAX / 4)
+    if (!launchable((int64_t)n_seqs * H, kGdDecodeThreads))
         return fail(KDA_ERR_INVALID, "%s: n_seqs * H too large (%lld)", who, (long long)n_seqs * H);
     if (!std::isfinite(scale)) return fail(KDA_ERR_INVALID, "%s: scale is not finite", who);
     if (n_seqs == 0 || n_tokens == 0) return KDA_OK;

@@ -629,7 +629,8 @@ __device__ __forceinline__ void produce(const GdWork& w, Lds<OUT>& lds, int lane
 }
 
 template <bool OUT>
-constexpr int kThreads = 64 * (4 + (OUT ? 4 : 8));
+constexpr int kThreads = OUT ? kGdThreads : kGdSegmentThreads;
+static_assert(kThreads<true> == 64 * (4 + 4) && kThreads<false> == 64 * (4 + 8));
 
 template <bool OUT>
 __global__ __launch_bounds__(kThreads<OUT>) void gd_prefill(GdArgs a) {
@@ -797,7 +798,7 @@ __global__ __launch_bounds__(kThreads<OUT>) void gd_prefill(GdArgs a) {
 // (splitting M here or three steps ahead made no difference to either).
 constexpr int CSTR = D + 8;  // bf16 per column of the carry in LDS
 constexpr int AHEAD = 2;
-__global__ __launch_bounds__(512) void gd_merge(GdMergeArgs a) {
+__global__ __launch_bounds__(kGdMergeThreads) void gd_merge(GdMergeArgs a) {
     __shared__ __align__(16) uint16_t carry[2][2][16 * CSTR];  // [step parity][hi, lo]
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, gg = lane >> 4, m = lane & 15;
     // the column tiles of a head are n_items * H apart: with a multiple of 8
@@ -892,10 +893,10 @@ __global__ __launch_bounds__(512) void gd_merge(GdMergeArgs a) {
 // 32 heads (128 MiB), 62 against 70 for 80. Where a call finds the states of
 // the one before, it costs: 49 against 43, 60 against 53, and 196 against 217
 // from 352 MiB on.
-constexpr int DEC_W = 4;  // wavefronts (32-column tiles) per workgroup
+static_assert(kGdDecodeThreads == 64 * 4);  // a wavefront per 32-column tile
 
 template <bool NT>
-__global__ __launch_bounds__(64 * DEC_W) void gd_decode(GdDecodeArgs a) {
+__global__ __launch_bounds__(kGdDecodeThreads) void gd_decode(GdDecodeArgs a) {
     const int lane = threadIdx.x & 63, tile = threadIdx.x >> 6;
     const int64_t nh = blockIdx.x;
     const int64_t n = nh / a.H;
@@ -997,12 +998,13 @@ hipError_t launch_gd_prefill(const GdArgs& a, bool with_out, hipStream_t s) {
 }
 
 hipError_t launch_gd_merge(const GdMergeArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL(gd_merge, dim3((unsigned)(a.n_items * a.H * 8)), dim3(512), 0, s, a);
+    hipLaunchKernelGGL(gd_merge, dim3((unsigned)(a.n_items * a.H * kGdMergeTiles)), dim3(kGdMergeThreads),
+                       0, s, a);
     return hipGetLastError();
 }
 
 hipError_t launch_gd_decode(const GdDecodeArgs& a, hipStream_t s) {
-    const dim3 grid((unsigned)(a.n_seqs * a.H)), block(64 * DEC_W);
+    const dim3 grid((unsigned)(a.n_seqs * a.H)), block(kGdDecodeThreads);
     const bool nt = (size_t)a.n_seqs * a.H * (D * D * 4) > ((size_t)128 << 20);
     if (nt) hipLaunchKernelGGL(gd_decode<true>, grid, block, 0, s, a);
     else hipLaunchKernelGGL(gd_decode<false>, grid, block, 0, s, a);

@@ -8,6 +8,12 @@ namespace kda {
 
 constexpr int kGdChunk = 32;  // tokens per chunk of the gated delta prefill
 
+// Threads of a workgroup: the prefill's (one per unit and head) with output and
+// for a segment's end state and transfer, the merge's (kGdMergeTiles per
+// sequence and head) and the decode's (one per sequence and head).
+constexpr int kGdThreads = 512, kGdSegmentThreads = 768, kGdMergeThreads = 512, kGdDecodeThreads = 256;
+constexpr int kGdMergeTiles = 8;
+
 // A run of tokens of one sequence, advanced by one workgroup per head. `in` and
 // `out` name the state it starts from and where its end state goes.
 struct GdUnit {

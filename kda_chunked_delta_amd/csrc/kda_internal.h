@@ -20,6 +20,8 @@ kda_status hip_fail(hipError_t e, const char* what);
 // Whether [a, a + na) and [b, b + nb) share a byte (NULL or empty: never).
 bool overlap(const void* a, size_t na, const void* b, size_t nb);
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+// Whether a grid of this many workgroups can be launched: HIP takes fewer than 2^32 threads.
+inline bool launchable(int64_t workgroups, int threads) { return workgroups <= (int64_t)UINT32_MAX / threads; }
 
 // Makes a device current for a scope.
 struct DeviceScope {

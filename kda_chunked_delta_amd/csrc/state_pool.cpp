@@ -192,7 +192,8 @@ kda_status kda_beam_reorder_validate(const kda_pool* pool, const int32_t* slots,
         return fail(KDA_ERR_INVALID, "%s: batch must be >= 0 and beams in [1, %d] (got %d, %d)", who, kBeamMax, batch,
                     beams);
     const int64_t items = (int64_t)batch * beams;
-    if (items > INT32_MAX || items * (pool->page_bytes / 16384 + 1) > INT32_MAX)
+    const int64_t parts = (pool->page_bytes + kMovePart - 1) / kMovePart;  // up to 2^26
+    if (items > INT32_MAX || !launchable(items * parts, kMoveThreads))
         return fail(KDA_ERR_INVALID, "%s: batch * beams * page_bytes too large", who);
     const size_t n = (size_t)items * 4;
     const Buffer b[] = {{slots, n, "slots"}, {parents, n, "parents"}, {new_slots, n, "new_slots"}};
@@ -248,7 +249,7 @@ kda_status kda_beam_select_validate(int32_t batch, int32_t beams, int32_t vocab,
     const int64_t rows = (int64_t)batch * beams;
     int32_t chunk, splits;
     beam_split(rows, vocab, n, &chunk, &splits);
-    if (rows * splits > INT32_MAX || rows > INT32_MAX / 64 || (int64_t)beams * splits > 24 * 1024)
+    if (!launchable(rows * splits, kBeamThreads) || (int64_t)beams * splits > 24 * 1024)
         return fail(KDA_ERR_INVALID, "%s: batch * beams * vocab too large", who);
     const size_t size = dtype == KDA_FP32 ? 4 : 2, R = (size_t)rows, K = (size_t)batch * n;
     const Buffer b[] = {{out_scores, K * 4, "out_scores"}, {out_parents, K * 4, "out_parents"},

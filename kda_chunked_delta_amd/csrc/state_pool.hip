@@ -9,18 +9,16 @@ namespace {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-// Bytes copied by one workgroup at a time: 256 threads, 4 vectors each in
-// flight.
-constexpr int MOVE_VEC = 4;
-constexpr int MOVE_PART = 256 * 16 * MOVE_VEC;
+// A workgroup copies kMovePart bytes at a time: 4 vectors per thread in flight.
+constexpr int MOVE_VEC = kMovePart / (kMoveThreads * 16);
 
-// Part `part` of one page to another, by 256 threads. Read and written with the
+// Part `part` of one page to another, by kMoveThreads threads. Read and written with the
 // nontemporal hint: 64 forks of 2 MiB pages (256 MiB moved) run at 5.6 TB/s, a
 // plain copy of the card at 5.1.
 __device__ __forceinline__ void move_part(const PoolView& p, int layer, int src, int dst, int part) {
     const uint8_t* s = p.base + layer * p.layer_stride + src * p.page_bytes;
     uint8_t* d = p.base + layer * p.layer_stride + dst * p.page_bytes;
-    const int64_t at = (int64_t)part * MOVE_PART + threadIdx.x * 16;
+    const int64_t at = (int64_t)part * kMovePart + threadIdx.x * 16;
     u32x4 x[MOVE_VEC];
 #pragma unroll
     for (int i = 0; i < MOVE_VEC; ++i)
@@ -32,7 +30,7 @@ __device__ __forceinline__ void move_part(const PoolView& p, int layer, int src,
 
 __device__ __forceinline__ bool in_pool(const PoolView& p, int page) { return page >= 0 && page < p.n_pages; }
 
-__global__ __launch_bounds__(256) void pool_move(PoolView p, const int32_t* src, const int32_t* dst, int32_t n,
+__global__ __launch_bounds__(kMoveThreads) void pool_move(PoolView p, const int32_t* src, const int32_t* dst, int32_t n,
                                                  int32_t parts) {
     const int64_t per = (int64_t)parts * p.n_layers, total = per * n;
     for (int64_t f = blockIdx.x; f < total; f += gridDim.x) {
@@ -218,7 +216,7 @@ __global__ __launch_bounds__(1024) void pool_compact_plan(uint8_t* used, int32_t
 // not) are disjoint. One workgroup per part of one beam's page; each works the
 // plan of its batch entry out for itself, one beam per lane, which costs less
 // than a launch of its own. 16 entries of 4 beams and 32 heads: 25 us, 5.2 TB/s.
-__global__ __launch_bounds__(256) void beam_reorder(PoolView p, const int32_t* slots, const int32_t* parents,
+__global__ __launch_bounds__(kMoveThreads) void beam_reorder(PoolView p, const int32_t* slots, const int32_t* parents,
                                                     int32_t* new_slots, int32_t beams, int32_t parts) {
     __shared__ int32_t s_target;
     const int item = blockIdx.x / parts, part = blockIdx.x % parts;
@@ -255,7 +253,7 @@ __global__ __launch_bounds__(256) void beam_reorder(PoolView p, const int32_t* s
     for (int layer = 0; layer < p.n_layers; ++layer) move_part(p, layer, from, to, part);
 }
 
-int parts_of(const PoolView& p) { return (int)((p.page_bytes + MOVE_PART - 1) / MOVE_PART); }
+int parts_of(const PoolView& p) { return (int)((p.page_bytes + kMovePart - 1) / kMovePart); }
 
 }  // namespace
 
@@ -263,7 +261,7 @@ hipError_t launch_pool_move(const PoolView& p, const int32_t* src, const int32_t
     const int parts = parts_of(p);
     const int64_t total = (int64_t)parts * p.n_layers * n;
     if (total == 0 || p.n_pages == 0) return hipSuccess;
-    hipLaunchKernelGGL(pool_move, dim3((unsigned)(total < 4096 ? total : 4096)), dim3(256), 0, s, p, src, dst, n,
+    hipLaunchKernelGGL(pool_move, dim3((unsigned)(total < 4096 ? total : 4096)), dim3(kMoveThreads), 0, s, p, src, dst, n,
                        parts);
     return hipGetLastError();
 }
@@ -291,7 +289,8 @@ hipError_t launch_pool_fork_plan(uint8_t* used, int32_t n_pages, const int32_t* 
 }
 
 hipError_t launch_pool_free(uint8_t* used, int32_t n_pages, const int32_t* pages, int32_t n, hipStream_t s) {
-    hipLaunchKernelGGL(pool_free, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, used, n_pages, pages, n);
+    hipLaunchKernelGGL(pool_free, dim3((unsigned)(((int64_t)n + 255) / 256)), dim3(256), 0, s, used, n_pages, pages,
+                       n);
     return hipGetLastError();
 }
 
@@ -304,8 +303,8 @@ hipError_t launch_pool_compact_plan(uint8_t* used, int32_t n_pages, int32_t* tab
 hipError_t launch_beam_reorder(const PoolView& p, const int32_t* slots, const int32_t* parents, int32_t* new_slots,
                                int32_t batch, int32_t beams, hipStream_t s) {
     const int parts = parts_of(p);
-    hipLaunchKernelGGL(beam_reorder, dim3((unsigned)((int64_t)batch * beams * parts)), dim3(256), 0, s, p, slots,
-                       parents, new_slots, beams, parts);
+    hipLaunchKernelGGL(beam_reorder, dim3((unsigned)((int64_t)batch * beams * parts)), dim3(kMoveThreads), 0, s, p,
+                       slots, parents, new_slots, beams, parts);
     return hipGetLastError();
 }
 

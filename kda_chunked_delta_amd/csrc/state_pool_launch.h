@@ -16,6 +16,9 @@ struct PoolView {
 
 constexpr int kPoolCopyMax = 1024;   // pairs of one pool copy
 constexpr int kPoolForkMax = 8192;   // requests of one fork
+constexpr int kMoveThreads = 256;    // threads of a workgroup that moves part of a page
+constexpr int kMovePart = kMoveThreads * 64;  // bytes of that part
+constexpr int kBeamThreads = 256;    // threads of a workgroup of the selection
 constexpr int kBeamMax = 64;         // beams of one batch entry
 constexpr int kBeamPickMax = 64;     // candidates selected per batch entry
 

@@ -1,5 +1,6 @@
 """GPU tests of what the gated delta rule, the state pool's pages and beam
-selection state about their limits: the bound of the selection's log-sum-exp."""
+selection state about their limits: the bound of the selection's log-sum-exp,
+and the largest launches."""
 import pytest
 import torch
 
@@ -45,3 +46,59 @@ def test_log_sum_exp_of_equal_logits(dtype, m, y, B, V, step):
     assert off <= 2e-7 + 2.0 ** -24 * abs(want)
     # equal candidates of equal beams: by beam, then by token
     assert parent.tolist() == [[0] * 3] * B and token.tolist() == [[0, step, 2 * step]] * B
+
+
+# ---------------------------------------------------------------------------
+# the largest launches: just below 2^32 threads
+# ---------------------------------------------------------------------------
+def test_prefill_of_65535_one_token_prompts():
+    """From a zero state, o = beta (q . k) v: one rounding, and the level of fp32 states."""
+    N, H = 65535, 128
+    say("case prefill, 65535 x 128 units")
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    q = torch.randn(N, 1, 128, generator=gen, device=DEV).bfloat16()
+    v = torch.empty(N, H, 128, dtype=torch.bfloat16, device=DEV).normal_(generator=gen)
+    g, beta = torch.full((N, H), -0.5, device=DEV), torch.rand(N, H, generator=gen, device=DEV)
+    o, _ = kda.gated_delta_prefill(q, q, v, g, beta, cu_seqlens_host=list(range(N + 1)), use_intracard_cp=False,
+                                   scale=1 / 128)
+    for i in (0, 1, 40000, N - 1):
+        want = (q[i].double() ** 2).sum() / 128 * beta[i].double()[:, None] * v[i].double()
+        assert ((o[i].double() - want).abs() <= (2.0 ** -8 + 1e-5) * want.abs()).all(), i
+
+
+def test_decode_of_2_24_minus_1_sequences():
+    """Only the first and the last have a slot; the outputs of the others are zero."""
+    N = (1 << 24) - 1
+    say("case decode, 2^24 - 1 sequences")
+    gen = torch.Generator(device=DEV).manual_seed(2)
+    x = torch.empty(N, 1, 128, dtype=torch.bfloat16, device=DEV).normal_(std=0.1, generator=gen)
+    g, beta = torch.full((N, 1), -0.1, device=DEV), torch.full((N, 1), 0.5, device=DEV)
+    slots = torch.full((N,), -1, dtype=torch.int32, device=DEV)
+    slots[0], slots[-1] = 1, 0
+    pool = torch.randn(2, 1, 128, 128, generator=gen, device=DEV)
+    state = pool.flip(0).contiguous()
+    o = kda.gated_delta_decode(x, x, x, g, beta, pool, slots=slots)
+    two = [t[[0, N - 1]].contiguous() for t in (x, x, x, g, beta)]
+    want = kda.gated_delta_decode(*two, state)
+    assert torch.equal(o[[0, N - 1]], want) and torch.equal(pool, state.flip(0))
+    o[0] = o[-1] = 0.0
+    assert not o.any()
+
+
+def test_selection_and_reordering_of_2_24_minus_1_rows():
+    B, V = (1 << 24) - 1, 8
+    say("case selection, 2^24 - 1 rows")
+    x = torch.zeros(B, 1, V, dtype=torch.bfloat16, device=DEV)
+    best = torch.arange(B, device=DEV) * 7 % V
+    x.view(B, V).scatter_(1, best[:, None], 1.0)
+    _, parents, tokens, _ = kda.beam_select(x, torch.zeros(B, 1, device=DEV), n=1)
+    assert torch.equal(tokens[:, 0], best.int()) and not parents.any()
+    say("case reordering, 2^24 - 2 beams")
+    B //= 2
+    pool = torch.arange(2 * B * 4, dtype=torch.int32, device=DEV).view(2 * B, 4)
+    slots = torch.arange(2 * B, dtype=torch.int32, device=DEV).view(B, 2)
+    new = kda.beam_reorder(pool, slots, torch.ones_like(slots))  # both beams continue the second
+    assert torch.equal(new, slots.flip(1))
+    odd = torch.arange(1, 2 * B, 2, device=DEV)
+    want = (odd[:, None] * 4 + torch.arange(4, device=DEV)).int()
+    assert torch.equal(pool.view(B, 2, 4), want[:, None].expand(B, 2, 4))
