@@ -49,7 +49,7 @@ __global__ __launch_bounds__(kMoveThreads) void pool_move(PoolView p, const int3
 // compiler spilled the vectors: 40 us for two pages of 2 MiB instead of 8).
 template <int J>
 __global__ __launch_bounds__(1024) void pool_copy(PoolView p, const int32_t* src, const int32_t* dst, int32_t n,
-                                                  int32_t parts, int32_t log_vecs) {
+                                                  int32_t first_part, int32_t parts, int32_t log_vecs) {
     __shared__ int32_t to[kPoolCopyMax], from[kPoolCopyMax];
     const int tid = threadIdx.x;
     int d = -1;
@@ -66,7 +66,7 @@ __global__ __launch_bounds__(1024) void pool_copy(PoolView p, const int32_t* src
     __syncthreads();
     if (tid < n) to[tid] = d;
     __syncthreads();
-    const int layer = blockIdx.x / parts, part = blockIdx.x % parts;
+    const int at_part = first_part + blockIdx.x, layer = at_part / parts, part = at_part % parts;
     uint8_t* base = p.base + layer * p.layer_stride;
     // vector f of the workgroup: pair f >> log_vecs, a row of consecutive vectors of its page
     const int64_t first = (int64_t)part << log_vecs;
@@ -274,12 +274,17 @@ hipError_t launch_pool_copy(const PoolView& p, const int32_t* src, const int32_t
                             ((p.page_bytes / 16 * p.n_layers) >> log_vecs) < 512))
         --log_vecs;
     const int64_t parts = ((p.page_bytes / 16 - 1) >> log_vecs) + 1;
-    const dim3 grid((unsigned)(parts * p.n_layers)), block(1024);
-    const int64_t vectors = (int64_t)n << log_vecs;
-    if (vectors <= 1024) hipLaunchKernelGGL(pool_copy<1>, grid, block, 0, s, p, src, dst, n, (int)parts, log_vecs);
-    else if (vectors <= 4096) hipLaunchKernelGGL(pool_copy<4>, grid, block, 0, s, p, src, dst, n, (int)parts, log_vecs);
-    else hipLaunchKernelGGL(pool_copy<8>, grid, block, 0, s, p, src, dst, n, (int)parts, log_vecs);
-    return hipGetLastError();
+    const int64_t vectors = (int64_t)n << log_vecs, total = parts * p.n_layers;
+    const auto kernel = vectors <= 1024 ? pool_copy<1> : vectors <= 4096 ? pool_copy<4> : pool_copy<8>;
+    // parts are apart from each other; a launch takes fewer than 2^32 threads (512 MiB in parts of 128 bytes)
+    constexpr int64_t MOST = UINT32_MAX / 1024;
+    for (int64_t first = 0; first < total; first += MOST) {
+        const dim3 grid((unsigned)(total - first < MOST ? total - first : MOST));
+        hipLaunchKernelGGL(kernel, grid, dim3(1024), 0, s, p, src, dst, n, (int)first, (int)parts, log_vecs);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 hipError_t launch_pool_fork_plan(uint8_t* used, int32_t n_pages, const int32_t* src, int32_t* dst, int32_t n,

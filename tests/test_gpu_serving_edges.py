@@ -102,3 +102,20 @@ def test_selection_and_reordering_of_2_24_minus_1_rows():
     odd = torch.arange(1, 2 * B, 2, device=DEV)
     want = (odd[:, None] * 4 + torch.arange(4, device=DEV)).int()
     assert torch.equal(pool.view(B, 2, 4), want[:, None].expand(B, 2, 4))
+
+
+def test_copy_of_large_pages_with_many_pairs():
+    """1024 pairs take parts of 128 bytes, more of them than one launch has workgroups."""
+    say("case copy, 520 MiB pages")
+    pool = torch.randint(0, 1 << 30, (3, 130 << 20), dtype=torch.int32, device=DEV,
+                         generator=torch.Generator(device=DEV).manual_seed(4))
+    old = pool.clone()
+    src, dst = torch.full((2, 1024), -1, dtype=torch.int32, device=DEV).unbind(0)
+    src[5], dst[5], src[1000], dst[1000] = 0, 2, 2, 0
+    kda.pool_copy(pool, src, dst)
+    assert torch.equal(pool, old[[2, 1, 0]])
+    # the same with the pages' bytes spread over layers
+    layers = old.view(3, 13, 10 << 20).transpose(0, 1).contiguous()
+    want = layers[:, [2, 1, 0]]
+    kda.pool_copy(layers, src, dst, page_dim=1)
+    assert torch.equal(layers, want)
