@@ -588,12 +588,13 @@ kda_status kda_beam_select_validate(int32_t batch, int32_t beams, int32_t vocab,
                                     const int32_t *out_tokens, const uint8_t *out_finished, const void *workspace,
                                     size_t workspace_bytes);
 
-/* Per-kernel timing of kda_prefill and kda_decode calls on this context: while enabled,
+/* Per-kernel timing of the calls on this context (kda_prefill_noalloc's aside): while enabled,
  * every call records HIP events around each of its launches on its stream.
  * kda_get_timing waits for all recorded events, and returns, per kernel name
  * (in order of first launch), the summed elapsed milliseconds and the number
  * of launches since the previous kda_get_timing or kda_set_timing call; it
- * then clears the log. Returns the number of names (<= max), or -1 on error. */
+ * then clears the log. Names beyond max are dropped (there are about thirty).
+ * Returns the number of names (<= max), or -1 on error. */
 kda_status kda_set_timing(kda_ctx *ctx, int enable);
 int32_t kda_get_timing(kda_ctx *ctx, const char **names, double *total_ms, int32_t *launches,
                        int32_t max);

@@ -199,12 +199,13 @@ class Context:
         _check(lib().kda_set_timing(self.handle, int(bool(enable))), "kda_set_timing")
 
     def timing(self):
-        """{kernel name: (total ms, launches)} of the prefill calls since the
-        last read (waits for them; clears the log)."""
-        names = (ctypes.c_char_p * 16)()
-        ms = (ctypes.c_double * 16)()
-        cnt = (ctypes.c_int32 * 16)()
-        n = lib().kda_get_timing(self.handle, names, ms, cnt, 16)
+        """{kernel name: (total ms, launches)} of the calls since the last read
+        (waits for them; clears the log)."""
+        most = 64  # the library has some thirty names
+        names = (ctypes.c_char_p * most)()
+        ms = (ctypes.c_double * most)()
+        cnt = (ctypes.c_int32 * most)()
+        n = lib().kda_get_timing(self.handle, names, ms, cnt, most)
         if n < 0:
             raise KDAError(5, "kda_get_timing: " + lib().kda_last_error().decode())
         return {names[i].decode(): (ms[i], cnt[i]) for i in range(n)}

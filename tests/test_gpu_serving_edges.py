@@ -1,10 +1,11 @@
 """GPU tests of what the gated delta rule, the state pool's pages and beam
 selection state about their limits: the bound of the selection's log-sum-exp,
-and the largest launches."""
+the largest launches, and the timing of a window with every kernel in it."""
 import pytest
 import torch
 
 import kda_chunked_delta_amd as kda
+from kda_inputs import draw, draw_decode
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -119,3 +120,43 @@ def test_copy_of_large_pages_with_many_pairs():
     want = layers[:, [2, 1, 0]]
     kda.pool_copy(layers, src, dst, page_dim=1)
     assert torch.equal(layers, want)
+
+
+# ---------------------------------------------------------------------------
+# per-kernel timing
+# ---------------------------------------------------------------------------
+def test_timing_lists_every_kernel_of_a_serving_window():
+    """A server's window runs more than twenty kernels by name; none is dropped."""
+    say("case timing")
+    H, d = 2, draw([700], 2, seed=1, device=DEV)
+    cu, xs = d["cu_seqlens_host"], [d[x] for x in ("q", "k", "v", "g", "beta")]
+    one = draw_decode(1, H, seed=2, device=DEV)
+    tok = [one[x] for x in ("q", "k", "v", "g", "beta")]
+    pool, used = torch.zeros(6, H, 128, 128, device=DEV), torch.tensor([True] * 3 + [False] * 3, device=DEV)
+    i = lambda *v: torch.tensor(v, dtype=torch.int32, device=DEV)
+    state = d["initial_state"].clone()
+    plans = [kda.plan(cu, H, device=DEV), kda.plan_segments(cu, H, 4, device=DEV), kda.plan_split(cu, H, [20], 4, device=DEV),
+             kda.plan_warm_cp(cu, H, 8, 2, device=DEV)]
+    gated = kda.plan_gated_delta(cu, H, True, 4, device=DEV)
+    ctx = kda.context(DEV)
+    ctx.set_timing(True)
+    try:
+        ctx.timing()
+        for p in plans:
+            kda.prefill(*xs[:4], xs[4].bfloat16(), cu_seqlens_host=cu, plan=p, output_final_state=True)
+        kda.decode(*tok, state)
+        kda.gated_delta_prefill(*xs[:3], xs[3][..., 0].contiguous(), xs[4], cu_seqlens_host=cu, plan=gated)
+        kda.gated_delta_decode(*tok[:3], tok[3][..., 0].contiguous(), tok[4], state)
+        kda.beam_select(torch.zeros(1, 2, 50, device=DEV), torch.zeros(1, 2, device=DEV))
+        kda.beam_reorder(pool, i(0, 1).view(1, 2), i(1, 1).view(1, 2))
+        kda.pool_copy(pool, i(0), i(1))
+        kda.pool_fork(pool, used, i(0))
+        kda.pool_free(used, i(1))
+        kda.pool_compact(pool, used)
+        t = ctx.timing()
+    finally:
+        ctx.set_timing(False)
+    want = ["decode", "gated_delta_segments", "gated_delta_merge", "gated_delta", "gated_delta_decode", "beam_rows",
+            "beam_pick", "beam_reorder", "pool_copy", "pool_fork_plan", "pool_move", "pool_free", "pool_compact_plan"]
+    assert len(t) > 20 and not [n for n in want if n not in t], sorted(t)
+    assert t["pool_move"][1] == 2 and all(ms > 0 and n > 0 for ms, n in t.values())
