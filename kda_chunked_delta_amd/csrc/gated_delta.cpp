@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstring>
 #include <functional>
+#include <memory>
 #include <new>
 #include <queue>
 
@@ -121,7 +122,7 @@ kda_status build(int32_t n_cus, const int32_t* cu, int32_t n_seqs, int32_t H, in
             if (mode == KDA_CP_AUTO && 0.93 * t_serial <= t_cp) seg = 0;
         }
     }
-    kda_plan* p = new kda_plan();
+    auto p = std::make_unique<kda_plan>();
     p->gated = true;
     p->cu.assign(cu, cu + n_seqs + 1);
     int n_carry = 0, n_sum = 0, n_cp = 0;
@@ -162,9 +163,8 @@ kda_status build(int32_t n_cus, const int32_t* cu, int32_t n_seqs, int32_t H, in
     if (!launchable((int64_t)p->gd_units.size() * H, kGdThreads) ||
         !launchable((int64_t)p->gd_pre.size() * H, kGdSegmentThreads) ||
         !launchable((int64_t)p->gd_merges.size() * H * kGdMergeTiles, kGdMergeThreads)) {
-        const size_t n_units = p->gd_units.size();
-        delete p;
-        return fail(KDA_ERR_INVALID, "kda_plan_gated_delta: too many work units (%zu units, %d heads)", n_units, H);
+        return fail(KDA_ERR_INVALID, "kda_plan_gated_delta: too many work units (%zu units, %d heads)",
+                    p->gd_units.size(), H);
     }
     p->off_b = 0;
     p->off_carry = (size_t)n_sum * H * kStateBytes;
@@ -187,7 +187,7 @@ kda_status build(int32_t n_cus, const int32_t* cu, int32_t n_seqs, int32_t H, in
     in.est_serial_us = t_serial;
     in.est_cp_us = t_cp;
     in.est_split_us = in.est_warm_cp_us = -1.0;
-    *out = p;
+    *out = p.release();
     return KDA_OK;
 }
 
@@ -241,11 +241,10 @@ kda_status kda_plan_gated_delta(kda_ctx* ctx, const int32_t* cu_seqlens_host, in
     try {
         kda_status st = build(ctx->n_cus, cu_seqlens_host, n_seqs, H, dk, dv, mode, seg_chunks, out);
         if (st != KDA_OK) return st;
-        st = upload(*out, ctx->device);
-        if (st != KDA_OK) {
-            delete *out;
-            *out = nullptr;
-        }
+        std::unique_ptr<kda_plan> p(*out);
+        *out = nullptr;
+        st = upload(p.get(), ctx->device);
+        if (st == KDA_OK) *out = p.release();
         return st;
     } catch (const std::bad_alloc&) {
         return fail(KDA_ERR_INVALID, "kda_plan_gated_delta: out of host memory");

@@ -2,6 +2,9 @@
 pool's pages and beam selection: HIP launches fewer than 2^32 threads, and what
 would need more is refused by the checks of arguments."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 
@@ -58,3 +61,25 @@ def test_selected_chunks(kda_lib, B, W, V, n, fits):
     need = kda_lib.kda_beam_select_workspace_bytes(B, W, V, n)
     st = kda_lib.kda_beam_select_validate(B, W, V, n, a[0], 1, V, a[1], None, -1, a[2], a[3], a[4], None, a[5], need)
     assert st == (OK if fits else INVALID)
+
+
+OUT_OF_MEMORY = """
+import ctypes, resource, sys
+import kda_chunked_delta_amd as kda
+kda.plan_gated_delta_host([0, 4096], 1, 256, True, 1)
+size = lambda: int(open("/proc/self/statm").read().split()[0]) * resource.getpagesize()
+before = size()
+resource.setrlimit(resource.RLIMIT_AS, (before + (200 << 20),) * 2)
+cu, h = (ctypes.c_int32 * 2)(0, 1 << 28), ctypes.c_void_p()
+st = kda.lib().kda_plan_gated_delta_host(256, cu, 1, 1, 128, 128, 1, 1, ctypes.byref(h))
+print(st, bool(h), size() - before >> 20, kda.lib().kda_last_error().decode())
+"""
+
+
+def test_a_plan_that_runs_out_of_memory_gives_it_back(kda_lib):
+    """Eight million segments of a chunk in 200 MiB: an error, and nothing kept."""
+    r = subprocess.run([sys.executable, "-c", OUT_OF_MEMORY], capture_output=True, text=True, timeout=100,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    status, plan, kept, message = r.stdout.strip().split(" ", 3)
+    assert int(status) == INVALID and plan == "False" and "memory" in message, (r.stdout, r.stderr)
+    assert int(kept) < 32, r.stdout
