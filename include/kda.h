@@ -421,10 +421,15 @@ kda_status kda_debug_k1_records(kda_ctx *ctx, const kda_plan *plan, const void *
  *   S_t = (I - beta_t k_t k_t^T) exp(g_t) S_{t-1} + beta_t k_t v_t^T,
  *   o_t = scale * S_t^T q_t,
  * over the same packed layouts and states, with g: fp32 [Tt, H] (g <= 0
- * expected; -inf forgets the state). Products are taken with the state and the
- * other computed operands as pairs of bf16 numbers, so an fp32 state is within
- * about 1e-5 of the exact one relative to its norm; bf16 outputs and states
- * are rounded once.
+ * expected; -inf forgets the state). The prefill's products are taken with the
+ * state and the other computed operands as pairs of bf16 numbers (16 bits of
+ * mantissa, sums in fp32): an fp32 state is within 1e-5 of the exact one
+ * relative to its norm (3e-6 to 6e-6 measured, plain fp32 arithmetic is within
+ * about 2e-7); bf16 outputs and states are rounded once. Decoding is fp32
+ * throughout. All other inputs have to be finite. A value of the prefill's that
+ * is not reaches the results of its own sequence and head from its chunk of 32
+ * tokens on, that is also of up to 31 tokens before it (one in v or a state:
+ * those of its own value column).
  * ------------------------------------------------------------------------- */
 
 /* Build the plan of a packed batch for kda_gated_delta_prefill. mode OFF runs
@@ -434,7 +439,7 @@ kda_status kda_debug_k1_records(kda_ctx *ctx, const kda_plan *plan, const void *
  * faster (few heads, long sequences). A segment's end state from zero and its
  * transfer matrix are formed first, the states between segments merged from
  * them, and all segments then run side by side; the results differ from the
- * unsegmented ones by fp32-level rounding. Errors and the upload of the
+ * unsegmented ones by the error of the pairs (1e-5 of a state's norm at most). Errors and the upload of the
  * tables are as in kda_plan_prefill; H is at most 131072, and H times the
  * sequences and segments below 2^23 (what one launch takes; forced segments a
  * little less). The plan is only accepted by kda_gated_delta_prefill, and the inspection calls. */
@@ -558,8 +563,9 @@ typedef enum { KDA_FP32 = 0, KDA_BF16 = 1, KDA_FP16 = 2 } kda_dtype;
 /* Beam search's selection. For beam w of batch entry b, candidate token t has
  * the value scores[b, w] + log_softmax(logits[b, w])[t]. The n candidates of
  * highest value over the beams and the vocabulary are selected per batch entry, in the
- * order of value; the candidates of one beam go by logit, then by the lower t,
- * equal values of two beams by the lower w.
+ * order of value; the candidates of one beam go by logit, then by the lower t (by t
+ * alone where the beam's score is -inf, or the beam finished), equal values of two
+ * beams by the lower w.
  *   logits  : [batch * beams] rows of vocab elements, row_stride elements apart
  *             (aligned to an element)
  *   scores  : fp32 [batch, beams]

@@ -593,8 +593,9 @@ def gated_delta_prefill(q, k, v, g, beta, cu_seqlens=None, initial_state=None, o
     [B, T, H]); beta: fp32 or bf16, same shape. Grouped value heads,
     cu_seqlens, the states, scale, out and the returned (o, final_state or
     None) are as in prefill. use_intracard_cp: "auto" cuts long sequences with
-    few heads into segments (equal up to fp32-level rounding), False never
-    does. plan: from plan_gated_delta; made on the first call with these
+    few heads into segments (equal within 1e-5 of a state's norm), False never
+    does. Inputs have to be finite (but g may be -inf): the results of a head
+    are not from the 32-token chunk of a value on that is not. plan: from plan_gated_delta; made on the first call with these
     cu_seqlens otherwise, which a graph capture cannot. The workspace of a
     segmented plan comes from torch's allocator, on the current stream.
     """
@@ -850,7 +851,8 @@ def beam_select(logits, scores, n=None, finished=None, eos=None):
     even distance (a slice of a padded vocabulary is fine); scores: fp32
     [B, W] running log-probabilities. Candidate (w, t) has the value
     scores[w] + log_softmax(logits[w])[t]; the candidates of one beam go by
-    logit, then by the lower t, equal values of two beams by the lower w.
+    logit, then by the lower t (by t alone where the score is -inf), equal
+    values of two beams by the lower w.
     n: candidates per batch entry (default W; at most 64). finished: bool
     [B, W], needs eos: such a beam has the single candidate eos, at its own
     score. NaN counts as -inf. Returns (scores [B, n] fp32, parents [B, n]

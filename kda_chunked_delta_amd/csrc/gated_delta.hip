@@ -15,7 +15,9 @@
 // numbers hi + lo, which carries 16 bits of mantissa; products of two such
 // pairs leave out lo * lo (2^-18 of the product). All sums are fp32, the
 // running sum of g is fp64 (differences of it are taken), so states keep about
-// 2^-18 per step against the 2^-9 of single bf16 operands.
+// 2^-18 per step against the 2^-9 of single bf16 operands. Zeros of L, T' and A
+// multiply whatever is there: a value that is not finite reaches all rows of its
+// chunk.
 #include "gated_delta_launch.h"
 #include "kda_device.hpp"
 

@@ -1,6 +1,7 @@
 """GPU tests of what the gated delta rule, the state pool's pages and beam
 selection state about their limits: the bound of the selection's log-sum-exp,
-the largest launches, and the timing of a window with every kernel in it."""
+the largest launches, the timing of a window with every kernel in it, how far a
+value that is not finite reaches, and the order of candidates at -inf."""
 import pytest
 import torch
 
@@ -160,3 +161,54 @@ def test_timing_lists_every_kernel_of_a_serving_window():
             "beam_pick", "beam_reorder", "pool_copy", "pool_fork_plan", "pool_move", "pool_free", "pool_compact_plan"]
     assert len(t) > 20 and not [n for n in want if n not in t], sorted(t)
     assert t["pool_move"][1] == 2 and all(ms > 0 and n > 0 for ms, n in t.values())
+
+
+# ---------------------------------------------------------------------------
+# values that are not finite
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("seg", [0, 1])
+def test_prefill_with_a_value_that_is_not_finite(value, seg):
+    """One in v reaches its own value column of its head from its chunk of 32 on;
+    one in k its head from there on. Every other result keeps its bits."""
+    say("case not finite", value, seg)
+    d = draw([100, 70], 3, seed=11, device=DEV)
+    xs = [d[x] for x in ("q", "k", "v", "g", "beta")]
+    xs[3] = xs[3][..., 0].contiguous()
+    plan = kda.plan_gated_delta(d["cu_seqlens_host"], 3, seg > 0, seg, device=DEV)
+    run = lambda: kda.gated_delta_prefill(*xs, cu_seqlens_host=d["cu_seqlens_host"], plan=plan,
+                                          initial_state=d["initial_state"], output_final_state=True)
+    o, s = run()
+    for at, column in ((2, 7), (1, None)):
+        old = xs[at].clone()
+        xs[at][45, 1, 7] = value
+        o2, s2 = run()
+        xs[at].copy_(old)
+        hit_o, hit_s = torch.zeros_like(o, dtype=torch.bool), torch.zeros_like(s, dtype=torch.bool)
+        hit_o[32:100, 1, slice(None) if column is None else slice(column, column + 1)] = True
+        hit_s[0, 1, :, slice(None) if column is None else slice(column, column + 1)] = True
+        assert torch.equal(o2[~hit_o], o[~hit_o]) and torch.equal(s2[~hit_s], s[~hit_s])
+        tail = o2[45:100, 1] if column is None else o2[45:100, 1, column]
+        assert not torch.isfinite(tail).any() and not torch.isfinite(s2[hit_s]).any()
+        again, s3 = run()  # nothing of it is left behind
+        assert torch.equal(again, o) and torch.equal(s3, s)
+
+
+@pytest.mark.parametrize("V", [40, 9000, 300000])
+def test_order_of_candidates_at_minus_infinity(V):
+    """A beam at score -inf gives its tokens in order; a finite one, with logits
+    at +inf that share the row, the others by logit."""
+    say("case -inf", V)
+    gen = torch.Generator(device=DEV).manual_seed(V)
+    x = torch.randperm(V, generator=gen, device=DEV).float().sub(V // 2).view(1, 1, V).repeat(2, 2, 1)
+    x[1, :, [30, 11]] = float("inf")
+    score = torch.tensor([[-float("inf"), -float("inf")], [-1.0, -float("inf")]], device=DEV)
+    s, parents, tokens, _ = kda.beam_select(x, score, n=6)
+    assert not parents.any()
+    assert tokens[0].tolist() == list(range(6)) and torch.isneginf(s[0]).all()
+    rest = x[1, 0].clone()
+    rest[[30, 11]] = -float("inf")
+    assert tokens[1].tolist() == [11, 30] + rest.argsort(descending=True)[:4].tolist()
+    want = torch.tensor(-1.0 - 0.6931471805599453, dtype=torch.float64)
+    assert ((s[1, :2].cpu().double() - want).abs() <= 2e-7 + 2.0 ** -24 * want.abs()).all()
+    assert torch.isneginf(s[1, 2:]).all()
