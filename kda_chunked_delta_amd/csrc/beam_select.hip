@@ -139,8 +139,9 @@ __device__ __forceinline__ uint64_t nth_key(uint32_t value, uint32_t token, int 
 // keys, and only n groups have keys at or above it: those (at most 4 n N, in
 // practice little more than n) are ranked by counting.
 //
-// Measured on 32 x 8 rows of 131072 bf16 logits, n = 16 (67 MB): 26 us, 2.6 TB/s,
-// half of it the stream and half the edge and the exponentials (71 us with the
+// Measured on 32 x 8 rows of 131072 bf16 logits, n = 16 (67 MB): 28 us, 2.4 TB/s,
+// half of it the stream and half vector instructions: the exponentials, the
+// first keys (a compare and two selects per logit) and the edge (71 us with the
 // edge from ranks over all 256 threads' first keys). Every load of a thread is
 // in flight at once.
 template <int DT, int VECS>

@@ -67,7 +67,8 @@ kda_status on_device(kda_ctx* ctx, hipStream_t stream, const char* who, F&& body
 // chip with fewer than two workgroups per compute unit, or where the room for
 // a chunk's candidates (4 n per element and thread) would pass 32 KiB. Measured,
 // both kernels, 8192 and 2048: 4 rows of 32000, 20 and 16 us; 128 rows, 18 and
-// 18; 256 rows of 131072, 39 and 108.
+// 18; 256 rows of 131072, 39 and 108. The rule looks at beam_rows alone: 8 to 24
+// rows of 131072 get 64 chunks each, which beam_pick cannot stage (39 to 67 us).
 void beam_split(int64_t rows, int64_t vocab, int32_t n, int32_t* chunk, int32_t* splits) {
     *chunk = n <= 32 && rows * ((vocab + 8191) / 8192) >= 512 ? 8192 : 2048;
     *splits = (int32_t)((vocab + *chunk - 1) / *chunk);

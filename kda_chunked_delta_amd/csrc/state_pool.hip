@@ -13,8 +13,8 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 constexpr int MOVE_VEC = kMovePart / (kMoveThreads * 16);
 
 // Part `part` of one page to another, by kMoveThreads threads. Read and written with the
-// nontemporal hint: 64 forks of 2 MiB pages (256 MiB moved) run at 5.6 TB/s, a
-// plain copy of the card at 5.1.
+// nontemporal hint: 64 forks of 2 MiB pages (256 MiB moved) take 43 us, 6.2 TB/s,
+// where a plain copy of 1 GiB runs at 5.2.
 __device__ __forceinline__ void move_part(const PoolView& p, int layer, int src, int dst, int part) {
     const uint8_t* s = p.base + layer * p.layer_stride + src * p.page_bytes;
     uint8_t* d = p.base + layer * p.layer_stride + dst * p.page_bytes;
@@ -47,6 +47,8 @@ __global__ __launch_bounds__(kMoveThreads) void pool_move(PoolView p, const int3
 // destination the last wins. Vectors that nothing is copied from are read from
 // the pool's first bytes, so that the loads need no branches (with them the
 // compiler spilled the vectors: 40 us for two pages of 2 MiB instead of 8).
+// Rotations of 2 MiB pages: 16 in 11.5 us, 64 in 37, and 256, in parts of 512
+// bytes, in 269 (4.0 TB/s).
 template <int J>
 __global__ __launch_bounds__(1024) void pool_copy(PoolView p, const int32_t* src, const int32_t* dst, int32_t n,
                                                   int32_t first_part, int32_t parts, int32_t log_vecs) {
