@@ -134,7 +134,7 @@ kda_status build(int32_t n_cus, const int32_t* cu, int32_t n_seqs, int32_t H, in
         }
         for (int s = 0; s < n; ++s) {
             const int c0 = (int)((int64_t)nch[i] * s / n), c1 = (int)((int64_t)nch[i] * (s + 1) / n);
-            const int t0 = c0 * kGdChunk, nt = std::min(c1 * kGdChunk, L) - t0;
+            const int t0 = c0 * kGdChunk, nt = (int)(std::min((int64_t)c1 * kGdChunk, (int64_t)L) - t0);
             p->gd_units.push_back(GdUnit{i, t0, nt, n > 1 ? n_carry + s : GD_INITIAL, s + 1 == n ? GD_FINAL : GD_NONE,
                                          GD_NONE});
             if (s + 1 < n) {
@@ -180,8 +180,7 @@ kda_status build(int32_t n_cus, const int32_t* cu, int32_t n_seqs, int32_t H, in
     in.n_cp_seqs = n_cp;
     in.n_prescan = n_sum;
     in.n_carry_slots = n_carry;
-    for (const GdUnit& u : p->gd_units)
-        in.max_unit_chunks = std::max(in.max_unit_chunks, (u.n_tok + kGdChunk - 1) / kGdChunk);
+    in.max_unit_chunks = p->units[0].n_chunks;
     in.n_cus = n_cus;
     in.workspace_bytes = p->off_carry + (size_t)n_carry * H * kStateBytes;
     in.est_serial_us = t_serial;

@@ -83,3 +83,13 @@ def test_a_plan_that_runs_out_of_memory_gives_it_back(kda_lib):
     status, plan, kept, message = r.stdout.strip().split(" ", 3)
     assert int(status) == INVALID and plan == "False" and "memory" in message, (r.stdout, r.stderr)
     assert int(kept) < 32, r.stdout
+
+
+@pytest.mark.parametrize("tokens", [(1 << 31) - 1, (1 << 31) - 31, (1 << 31) - 32])
+@pytest.mark.parametrize("seg", [0, 1 << 22])
+def test_plan_of_the_longest_prompt(kda_lib, tokens, seg):
+    """Chunks whose end lies beyond 2^31 - 1 tokens."""
+    p = kda.plan_gated_delta_host([0, tokens], 1, 256, seg > 0, seg)
+    chunks = -(-tokens // 32)
+    assert sum(u["n_chunks"] for u in p.units()) == chunks == p.info()["total_chunks"]
+    assert p.info()["max_unit_chunks"] == max(u["n_chunks"] for u in p.units())
