@@ -496,6 +496,76 @@ kda_status kda_gated_delta_decode_validate(int32_t n_seqs, int32_t n_tokens, int
                                            const int32_t *slots, const void *out);
 
 /* ---------------------------------------------------------------------------
+ * Linear attention with one decay per head: the recurrence
+ *   S_t = exp(g_t) S_{t-1} + k_t v_t^T,   o_t = scale * S_t^T q_t,
+ * over the packed layouts and states of the gated delta rule, with a log-decay g
+ * (g <= 0 expected; -inf forgets the state) per token and head, or one per head
+ * for all tokens. In the prefill, sums are fp32 and what a token adds to the
+ * state enters as a pair of bf16 numbers (16 bits of mantissa): an fp32 state is
+ * within 1e-5 of the exact one relative to its norm. The state that an output
+ * reads and the decayed products q . k are rounded to bf16 once. Decoding is fp32
+ * throughout. All other inputs have to be finite: a value that is not reaches
+ * the results of its own sequence and head from its chunk of 32 tokens on, that
+ * is also of up to 31 tokens before it.
+ * ------------------------------------------------------------------------- */
+
+/* Build the plan of a packed batch for kda_linear_attention_prefill: as
+ * kda_plan_gated_delta, with the same modes, segments of chunks of 32 tokens,
+ * limits and errors. Segments are joined by their end states from zero and one
+ * decay per head; their results differ from the unsegmented ones by rounding in
+ * fp32. The plan is only accepted by kda_linear_attention_prefill, and the
+ * inspection calls. */
+kda_status kda_plan_linear_attention(kda_ctx *ctx, const int32_t *cu_seqlens_host, int32_t n_seqs, int32_t H,
+                                     int32_t dk, int32_t dv, kda_cp_mode mode, int32_t seg_chunks, kda_plan **out);
+
+/* The same for an explicit compute-unit count, host only (not executable). */
+kda_status kda_plan_linear_attention_host(int32_t n_cus, const int32_t *cu_seqlens_host, int32_t n_seqs, int32_t H,
+                                          int32_t dk, int32_t dv, kda_cp_mode mode, int32_t seg_chunks,
+                                          kda_plan **out);
+
+/* Options of kda_linear_attention_prefill. A zeroed struct (or NULL): as many
+ * q/k heads as value heads, g per token, fp32 states. */
+typedef struct {
+    int32_t qk_heads;   /* grouped value heads, as in kda_prefill_opts; 0 means H */
+    int32_t g_fixed;    /* 1: g is [H], the same for every token */
+    int32_t state_bf16; /* 1: initial_state and final_state are bf16, as in kda_prefill_opts */
+} kda_linear_opts;
+
+/* Run the prefill on `stream`.
+ *   q, k      : bf16 [Tt, qk_heads, 128] (device, 16-byte aligned)
+ *   v, out    : bf16 [Tt, H, 128] (device, 16-byte aligned)
+ *   g         : fp32 [Tt, H], or [H] with g_fixed (device, 4-byte aligned)
+ *   states, cu_seqlens_dev, scale and workspace as in kda_gated_delta_prefill
+ * The call allocates nothing and synchronises nothing. final_state may equal
+ * initial_state. Results are bitwise reproducible. */
+kda_status kda_linear_attention_prefill(kda_ctx *ctx, const kda_plan *plan, const kda_linear_opts *opts, const void *q,
+                                        const void *k, const void *v, const float *g, const int32_t *cu_seqlens_dev,
+                                        float scale, const void *initial_state, void *final_state, void *out,
+                                        void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* The argument checks of kda_linear_attention_prefill (addresses only; no GPU). */
+kda_status kda_linear_attention_prefill_validate(const kda_plan *plan, const kda_linear_opts *opts, const void *q,
+                                                 const void *k, const void *v, const float *g,
+                                                 const int32_t *cu_seqlens_dev, float scale,
+                                                 const void *initial_state, const void *final_state, const void *out,
+                                                 const void *workspace, size_t workspace_bytes);
+
+/* Decode: each of n_seqs sequences receives n_tokens new tokens, in order, and
+ * its state is advanced in place, as in kda_gated_delta_decode (the same layouts,
+ * slots, limits and errors, without beta). g: fp32 [n_seqs, n_tokens, H], or [H]
+ * with g_fixed. A call with n tokens gives the bits of n calls with one. */
+kda_status kda_linear_attention_decode(kda_ctx *ctx, int32_t n_seqs, int32_t n_tokens, int32_t H, int32_t qk_heads,
+                                       int32_t dk, int32_t dv, const void *q, const void *k, const void *v,
+                                       const float *g, int32_t g_fixed, float scale, float *state, int32_t n_slots,
+                                       const int32_t *slots, void *out, hipStream_t stream);
+
+/* The argument checks of kda_linear_attention_decode (addresses only; no GPU). */
+kda_status kda_linear_attention_decode_validate(int32_t n_seqs, int32_t n_tokens, int32_t H, int32_t qk_heads,
+                                                int32_t dk, int32_t dv, const void *q, const void *k, const void *v,
+                                                const float *g, int32_t g_fixed, float scale, const float *state,
+                                                int32_t n_slots, const int32_t *slots, const void *out);
+
+/* ---------------------------------------------------------------------------
  * Pages of a state pool, and beam search over it. A page is one slot of a pool
  * of states [n_pages, H, 128, 128] (of kda_decode_slots or
  * kda_gated_delta_decode); with several layers it is that slot of each. All
@@ -593,6 +663,50 @@ kda_status kda_beam_select_validate(int32_t batch, int32_t beams, int32_t vocab,
                                     int32_t eos, const float *out_scores, const int32_t *out_parents,
                                     const int32_t *out_tokens, const uint8_t *out_finished, const void *workspace,
                                     size_t workspace_bytes);
+
+/* The processing of logits in front of a selection. For token t of a row, with
+ * n the number of times it stands in the row's history and m the number of those
+ * past the prompt, in this order:
+ *   n > 0 (repetition)          : x = x > 0 ? x / repetition : x * repetition
+ *   m > 0 (frequency, presence) : x = x - (frequency * m + presence)
+ *   t has a bias                : x = x + bias (of several the last one's)
+ *   t is not allowed            : x = -inf, whatever x is
+ * in fp32 (IEEE arithmetic, infinities and NaN included), rounded once to the
+ * logits' type. A logit that nothing applies to keeps its bits. Tokens outside
+ * [0, vocab) in a list (-1 for padding) are skipped. A row whose mask allows
+ * nothing becomes -inf. Pointers are device memory; each part may be left out
+ * (NULL, or a count of 0). Rows are strides (in elements) apart; a stride of 0
+ * gives all rows the same list or mask. */
+typedef struct {
+    int32_t rows, vocab;
+    kda_dtype dtype;               /* of logits and out */
+    const void *logits;            /* [rows, vocab], aligned to an element */
+    int64_t row_stride;            /* at least vocab */
+    void *out;                     /* [rows, vocab]: logits itself, or apart from every input */
+    int64_t out_stride;            /* at least vocab; row_stride in place */
+    const int32_t *tokens;         /* history [rows, max_tokens] */
+    int64_t token_stride;
+    int32_t max_tokens;            /* below 2^30 */
+    const int32_t *lengths;        /* [rows] tokens that count, cut to [0, max_tokens]; NULL: max_tokens */
+    const int32_t *prompt_lengths; /* [rows] how many of them, from the start, are the prompt; NULL: none */
+    const float *repetition;       /* [rows] */
+    const float *frequency;        /* [rows] */
+    const float *presence;         /* [rows] */
+    const int32_t *bias_tokens;    /* [rows, n_bias] */
+    const float *bias;             /* [rows, n_bias], bias_stride apart as the tokens */
+    int64_t bias_stride;
+    int32_t n_bias;
+    const uint32_t *allowed;       /* [rows, ceil(vocab / 32)]: bit t & 31 of word t >> 5 set for an allowed token */
+    int64_t allowed_stride;
+} kda_logits;
+
+/* One launch on `stream`, no workspace, no allocation, no synchronisation;
+ * results are bitwise reproducible. rows times the chunks of 2048 logits of a row
+ * are fewer than 2^24. */
+kda_status kda_logits_process(kda_ctx *ctx, const kda_logits *args, hipStream_t stream);
+
+/* The argument checks of kda_logits_process (addresses only; no GPU). */
+kda_status kda_logits_process_validate(const kda_logits *args);
 
 /* Per-kernel timing of the calls on this context (kda_prefill_noalloc's aside): while enabled,
  * every call records HIP events around each of its launches on its stream.

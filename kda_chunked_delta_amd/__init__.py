@@ -11,6 +11,8 @@ every entry point raises.
     o_t = kda.decode(q_t, k_t, v_t, g_t, beta_t, s)   # one token each, s in place
     o, s = kda.gated_delta_prefill(q, k, v, g1, beta, cu_seqlens=cu, output_final_state=True)
     o_t = kda.gated_delta_decode(q_t, k_t, v_t, g1_t, beta_t, s)   # g1: one decay per head
+    o, s = kda.linear_attention_prefill(q, k, v, g1, cu_seqlens=cu, output_final_state=True)
+    o_t = kda.linear_attention_decode(q_t, k_t, v_t, g1_t, s)
 
 The interface follows the FLA-compatible prefill of "feat(kda/sm90): FlashKDA
 prefill port + intracard-CP prefill" (cuLA pull request #103, description:
@@ -29,8 +31,9 @@ import threading
 
 __all__ = ["prefill", "decode", "plan", "plan_host", "plan_segments", "Plan", "Context", "context",
            "gated_delta_prefill", "gated_delta_decode", "plan_gated_delta", "plan_gated_delta_host",
-           "beam_select", "beam_reorder", "pool_copy", "pool_fork", "pool_free", "pool_compact",
-           "KDAError", "lib", "LIB_PATH", "CP_OFF", "CP_ON", "CP_AUTO"]
+           "linear_attention_prefill", "linear_attention_decode", "plan_linear_attention",
+           "plan_linear_attention_host", "logits_process", "beam_select", "beam_reorder", "pool_copy",
+           "pool_fork", "pool_free", "pool_compact", "KDAError", "lib", "LIB_PATH", "CP_OFF", "CP_ON", "CP_AUTO"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkda.so")
@@ -67,6 +70,20 @@ class PlanInfo(ctypes.Structure):
 
 class PrefillOpts(ctypes.Structure):
     _fields_ = [("qk_heads", ctypes.c_int32), ("beta_bf16", ctypes.c_int32), ("state_bf16", ctypes.c_int32)]
+
+
+class LinearOpts(ctypes.Structure):
+    _fields_ = [("qk_heads", ctypes.c_int32), ("g_fixed", ctypes.c_int32), ("state_bf16", ctypes.c_int32)]
+
+
+class Logits(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("vocab", ctypes.c_int32), ("dtype", ctypes.c_int),
+                ("logits", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("out_stride", ctypes.c_int64), ("tokens", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("max_tokens", ctypes.c_int32), ("lengths", ctypes.c_void_p), ("prompt_lengths", ctypes.c_void_p),
+                ("repetition", ctypes.c_void_p), ("frequency", ctypes.c_void_p), ("presence", ctypes.c_void_p),
+                ("bias_tokens", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("bias_stride", ctypes.c_int64),
+                ("n_bias", ctypes.c_int32), ("allowed", ctypes.c_void_p), ("allowed_stride", ctypes.c_int64)]
 
 
 class Pool(ctypes.Structure):
@@ -134,6 +151,18 @@ def lib():
                                                           P, P, P]),
                 "kda_gated_delta_decode_validate": (ctypes.c_int, [I32, I32, I32, I32, I32, I32, P, P, P, P, P, F32,
                                                                    P, I32, P, P]),
+                "kda_plan_linear_attention": (ctypes.c_int, [P, P, I32, I32, I32, I32, ctypes.c_int, I32, PP]),
+                "kda_plan_linear_attention_host": (ctypes.c_int, [I32, P, I32, I32, I32, I32, ctypes.c_int, I32, PP]),
+                "kda_linear_attention_prefill": (ctypes.c_int, [P, P, ctypes.POINTER(LinearOpts), P, P, P, P, P, F32, P,
+                                                                P, P, P, ctypes.c_size_t, P]),
+                "kda_linear_attention_prefill_validate": (ctypes.c_int, [P, ctypes.POINTER(LinearOpts), P, P, P, P, P,
+                                                                         F32, P, P, P, P, ctypes.c_size_t]),
+                "kda_linear_attention_decode": (ctypes.c_int, [P, I32, I32, I32, I32, I32, I32, P, P, P, P, I32, F32, P,
+                                                               I32, P, P, P]),
+                "kda_linear_attention_decode_validate": (ctypes.c_int, [I32, I32, I32, I32, I32, I32, P, P, P, P, I32,
+                                                                        F32, P, I32, P, P]),
+                "kda_logits_process": (ctypes.c_int, [P, ctypes.POINTER(Logits), P]),
+                "kda_logits_process_validate": (ctypes.c_int, [ctypes.POINTER(Logits)]),
                 "kda_pool_copy": (ctypes.c_int, [P, ctypes.POINTER(Pool), P, P, I32, P]),
                 "kda_pool_copy_validate": (ctypes.c_int, [ctypes.POINTER(Pool), P, P, I32]),
                 "kda_pool_fork": (ctypes.c_int, [P, ctypes.POINTER(Pool), P, P, P, I32, P]),
@@ -583,6 +612,47 @@ def _on(device):
     return _lib, ctx.handle, torch._C._cuda_getCurrentRawStream(device)
 
 
+def _packed_plan(what, make, plan, cu_seqlens, cu_seqlens_host, Tt, H, dev, use_intracard_cp, capturing):
+    """The plan of a packed call (given, cached or made), its cu_seqlens on the device, and the number of sequences."""
+    import torch
+    if cu_seqlens_host is None:
+        if cu_seqlens is None:
+            cu_seqlens_host = [0, Tt]
+        elif isinstance(cu_seqlens, (list, tuple)):
+            cu_seqlens_host = cu_seqlens
+        elif capturing:
+            raise ValueError("a graph capture needs cu_seqlens_host: device cu_seqlens cannot be read in it")
+        else:
+            cu_seqlens_host = cu_seqlens.tolist()  # host copy for the planner (synchronises)
+    cu_seqlens_host = [int(x) for x in cu_seqlens_host]
+    N = len(cu_seqlens_host) - 1
+    # the library sizes every buffer from the plan, so the table must describe
+    # exactly the packed tokens the tensors hold
+    if (N < 1 or cu_seqlens_host[0] != 0 or cu_seqlens_host[-1] != Tt
+            or any(b < a for a, b in zip(cu_seqlens_host, cu_seqlens_host[1:]))):
+        raise ValueError("cu_seqlens must start at 0, never decrease and end at the %d packed tokens (got %s)"
+                         % (Tt, cu_seqlens_host[:8]))
+    if plan is None:
+        mode = _cp_mode(use_intracard_cp)
+        if capturing and (dev, tuple(cu_seqlens_host), H, mode, make) not in _plan_cache:
+            raise ValueError("a graph capture needs a plan made before it: pass plan=plan_%s(...), or call "
+                             "once with these cu_seqlens" % what)
+        plan = _cached_plan(cu_seqlens_host, H, mode, dev, make)
+    elif plan.device != dev or plan.shape() != (H, Tt, N) or plan.cu_host != cu_seqlens_host:
+        raise ValueError("the plan was built for device %s, H=%d, %d tokens, %d sequences (cu_seqlens %s...); the call "
+                         "has device %s, H=%d, %d tokens, %d sequences"
+                         % (plan.device, *plan.shape(), plan.cu_host[:4], dev, H, Tt, N))
+    if cu_seqlens is None or isinstance(cu_seqlens, (list, tuple)):
+        if capturing and plan._cu_dev is None:
+            raise ValueError("a graph capture needs cu_seqlens on the device: pass them as a tensor, or call "
+                             "plan.cu_device() before it")
+        cu_dev = plan.cu_device()
+    else:
+        cu_dev = cu_seqlens
+        _need("cu_seqlens", cu_dev, torch.int32, (N + 1,), dev)
+    return plan, cu_dev, N
+
+
 def gated_delta_prefill(q, k, v, g, beta, cu_seqlens=None, initial_state=None, output_final_state=False,
                         use_intracard_cp="auto", scale=1.0, final_state=None, out=None, plan=None,
                         cu_seqlens_host=None, state_dtype=None):
@@ -625,41 +695,8 @@ def gated_delta_prefill(q, k, v, g, beta, cu_seqlens=None, initial_state=None, o
     _need("g", g, torch.float32, (Tt, H), dev)
     _need("beta", beta, torch.bfloat16 if beta16 else torch.float32, (Tt, H), dev)
     capturing = torch.cuda.is_current_stream_capturing()
-    if cu_seqlens_host is None:
-        if cu_seqlens is None:
-            cu_seqlens_host = [0, Tt]
-        elif isinstance(cu_seqlens, (list, tuple)):
-            cu_seqlens_host = cu_seqlens
-        elif capturing:
-            raise ValueError("a graph capture needs cu_seqlens_host: device cu_seqlens cannot be read in it")
-        else:
-            cu_seqlens_host = cu_seqlens.tolist()  # host copy for the planner (synchronises)
-    cu_seqlens_host = [int(x) for x in cu_seqlens_host]
-    N = len(cu_seqlens_host) - 1
-    # the library sizes every buffer from the plan, so the table must describe
-    # exactly the packed tokens the tensors hold
-    if (N < 1 or cu_seqlens_host[0] != 0 or cu_seqlens_host[-1] != Tt
-            or any(b < a for a, b in zip(cu_seqlens_host, cu_seqlens_host[1:]))):
-        raise ValueError("cu_seqlens must start at 0, never decrease and end at the %d packed tokens (got %s)"
-                         % (Tt, cu_seqlens_host[:8]))
-    if plan is None:
-        mode = _cp_mode(use_intracard_cp)
-        if capturing and (dev, tuple(cu_seqlens_host), H, mode, plan_gated_delta) not in _plan_cache:
-            raise ValueError("a graph capture needs a plan made before it: pass plan=plan_gated_delta(...), or call "
-                             "once with these cu_seqlens")
-        plan = _cached_plan(cu_seqlens_host, H, mode, dev, plan_gated_delta)
-    elif plan.device != dev or plan.shape() != (H, Tt, N) or plan.cu_host != cu_seqlens_host:
-        raise ValueError("the plan was built for device %s, H=%d, %d tokens, %d sequences (cu_seqlens %s...); the call "
-                         "has device %s, H=%d, %d tokens, %d sequences"
-                         % (plan.device, *plan.shape(), plan.cu_host[:4], dev, H, Tt, N))
-    if cu_seqlens is None or isinstance(cu_seqlens, (list, tuple)):
-        if capturing and plan._cu_dev is None:
-            raise ValueError("a graph capture needs cu_seqlens on the device: pass them as a tensor, or call "
-                             "plan.cu_device() before it")
-        cu_dev = plan.cu_device()
-    else:
-        cu_dev = cu_seqlens
-        _need("cu_seqlens", cu_dev, torch.int32, (N + 1,), dev)
+    plan, cu_dev, N = _packed_plan("gated_delta", plan_gated_delta, plan, cu_seqlens, cu_seqlens_host, Tt, H, dev,
+                                   use_intracard_cp, capturing)
     if state_dtype is None:
         given = initial_state if initial_state is not None else final_state
         state_dtype = given.dtype if given is not None else torch.float32
@@ -725,6 +762,133 @@ def gated_delta_decode(q, k, v, g, beta, state, scale=1.0, out=None, slots=None)
     _check(L.kda_gated_delta_decode(ctx, N, rows[1] if len(rows) == 2 else 1, H, Hk, D, D, q.data_ptr(), k.data_ptr(),
                                     v.data_ptr(), g.data_ptr(), beta.data_ptr(), float(scale), state.data_ptr(),
                                     n_slots, _addr(slots), out.data_ptr(), stream), "kda_gated_delta_decode")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# linear attention
+# ---------------------------------------------------------------------------
+def plan_linear_attention(cu_seqlens, H, use_intracard_cp="auto", seg_chunks=0, device=None):
+    """Executable plan of a linear attention prefill (arguments as in plan_gated_delta)."""
+    ctx = context(device)
+    arr, n = _cu_array(cu_seqlens)
+    h = ctypes.c_void_p()
+    _check(lib().kda_plan_linear_attention(ctx.handle, arr, n, int(H), D, D, _cp_mode(use_intracard_cp),
+                                           int(seg_chunks), ctypes.byref(h)), "kda_plan_linear_attention")
+    return Plan(h, cu_seqlens, ctx.device)
+
+
+def plan_linear_attention_host(cu_seqlens, H, n_cus, use_intracard_cp="auto", seg_chunks=0):
+    """The same for an explicit CU count (inspection; no GPU needed)."""
+    arr, n = _cu_array(cu_seqlens)
+    h = ctypes.c_void_p()
+    _check(lib().kda_plan_linear_attention_host(int(n_cus), arr, n, int(H), D, D, _cp_mode(use_intracard_cp),
+                                                int(seg_chunks), ctypes.byref(h)), "kda_plan_linear_attention_host")
+    return Plan(h, cu_seqlens)
+
+
+def linear_attention_prefill(q, k, v, g, cu_seqlens=None, initial_state=None, output_final_state=False,
+                             use_intracard_cp="auto", scale=1.0, final_state=None, out=None, plan=None,
+                             cu_seqlens_host=None, state_dtype=None):
+    """Linear attention forward prefill: S = exp(g) S + k v^T, o = scale S^T q.
+
+    q, k, v: bf16 [Tt, H, 128] packed, or [B, T, H, 128] (B equal-length
+    sequences when cu_seqlens is None); g: fp32 log-decay per token [Tt, H] (or
+    [B, T, H]), or [H] for one decay per head. Grouped value heads, cu_seqlens,
+    the states, scale, out, use_intracard_cp, plan (from plan_linear_attention),
+    graph capture and the returned (o, final_state or None) are as in
+    gated_delta_prefill. Inputs have to be finite (but g may be -inf).
+    """
+    import torch
+    if q.dim() == 4:
+        B, T = q.shape[0], q.shape[1]
+        if cu_seqlens is None and cu_seqlens_host is None:
+            cu_seqlens_host = [i * T for i in range(B + 1)]
+        elif B != 1:
+            raise ValueError("4-D inputs with cu_seqlens must have batch size 1")
+        flat = lambda x: x.reshape(B * T, *x.shape[2:])
+        if out is not None and not out.is_contiguous():
+            raise ValueError("out must be contiguous")
+        o, s = linear_attention_prefill(flat(q), flat(k), flat(v), g if g.dim() == 1 else flat(g), cu_seqlens,
+                                        initial_state, output_final_state, use_intracard_cp, scale, final_state,
+                                        None if out is None else flat(out), plan, cu_seqlens_host, state_dtype)
+        return o.view(v.shape), s
+    if q.dim() != 3 or q.shape[-1] != D or v.dim() != 3:
+        raise ValueError("q must be [Tt, H, 128] or [B, T, H, 128], got %s" % (tuple(q.shape),))
+    Tt, Hk, H, dev = q.shape[0], q.shape[1], v.shape[1], q.get_device()
+    if Hk < 1 or H < 1 or H % Hk:
+        raise ValueError("v has %d heads, not a multiple of the %d q/k heads" % (H, Hk))
+    fixed = g.dim() == 1
+    _need("q", q, torch.bfloat16, (Tt, Hk, D), dev)
+    _need("k", k, torch.bfloat16, (Tt, Hk, D), dev)
+    _need("v", v, torch.bfloat16, (Tt, H, D), dev)
+    _need("g", g, torch.float32, (H,) if fixed else (Tt, H), dev)
+    capturing = torch.cuda.is_current_stream_capturing()
+    plan, cu_dev, N = _packed_plan("linear_attention", plan_linear_attention, plan, cu_seqlens, cu_seqlens_host, Tt, H,
+                                   dev, use_intracard_cp, capturing)
+    if state_dtype is None:
+        given = initial_state if initial_state is not None else final_state
+        state_dtype = given.dtype if given is not None else torch.float32
+    if state_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("states must be fp32 or bf16, got %s" % (state_dtype,))
+    if initial_state is not None:
+        _need("initial_state", initial_state, state_dtype, (N, H, D, D), dev)
+    if final_state is not None:
+        _need("final_state", final_state, state_dtype, (N, H, D, D), dev)
+    elif output_final_state:
+        final_state = torch.empty(N, H, D, D, dtype=state_dtype, device=q.device)
+    if out is None:
+        out = torch.empty_like(v)
+    else:
+        _need("out", out, torch.bfloat16, (Tt, H, D), dev)
+    n_ws = plan.workspace_bytes()
+    ws = torch.empty(n_ws, dtype=torch.uint8, device=q.device) if n_ws else None
+    if capturing and not any(p is plan for p in _captured_plans):
+        _captured_plans.append(plan)
+    opts = LinearOpts(Hk, int(fixed), int(state_dtype == torch.bfloat16))
+    L, ctx, stream = _on(dev)
+    _check(L.kda_linear_attention_prefill(ctx, plan.handle, ctypes.byref(opts), q.data_ptr(), k.data_ptr(),
+                                          v.data_ptr(), g.data_ptr(), cu_dev.data_ptr(), float(scale),
+                                          _addr(initial_state), _addr(final_state), out.data_ptr(), _addr(ws), n_ws,
+                                          stream),
+           "kda_linear_attention_prefill")
+    return out, final_state
+
+
+def linear_attention_decode(q, k, v, g, state, scale=1.0, out=None, slots=None):
+    """Linear attention decode: new tokens per sequence, state advanced in place.
+
+    q, k, v: bf16 [N, H, 128] (one token each) or [N, T, H, 128] (T tokens
+    each, in order); g: fp32 log-decay [N, H] or [N, T, H], or [H] for one decay
+    per head; state: fp32 [N, H, 128, 128], overwritten. Grouped value heads,
+    slots and the returned o are as in gated_delta_decode.
+    """
+    import torch
+    if q.dim() not in (3, 4) or v.dim() != q.dim() or q.shape[-1] != D:
+        raise ValueError("q must be [N, H, 128] or [N, T, H, 128] (and v alike), got %s" % (tuple(q.shape),))
+    rows, Hk, H, dev = q.shape[:-2], q.shape[-2], v.shape[-2], q.get_device()
+    N = rows[0]
+    if Hk < 1 or H < 1 or H % Hk:
+        raise ValueError("v has %d heads, not a multiple of the %d q/k heads" % (H, Hk))
+    fixed = g.dim() == 1
+    _need("q", q, torch.bfloat16, (*rows, Hk, D), dev)
+    _need("k", k, torch.bfloat16, (*rows, Hk, D), dev)
+    _need("v", v, torch.bfloat16, (*rows, H, D), dev)
+    _need("g", g, torch.float32, (H,) if fixed else (*rows, H), dev)
+    n_slots = N
+    if slots is not None:
+        _need("slots", slots, torch.int32, (N,), dev)
+        n_slots = state.shape[0]
+    _need("state", state, torch.float32, (n_slots, H, D, D), dev)
+    if out is None:
+        out = torch.empty_like(v)
+    else:
+        _need("out", out, torch.bfloat16, v.shape, dev)
+    L, ctx, stream = _on(dev)
+    _check(L.kda_linear_attention_decode(ctx, N, rows[1] if len(rows) == 2 else 1, H, Hk, D, D, q.data_ptr(),
+                                         k.data_ptr(), v.data_ptr(), g.data_ptr(), int(fixed), float(scale),
+                                         state.data_ptr(), n_slots, _addr(slots), out.data_ptr(), stream),
+           "kda_linear_attention_decode")
     return out
 
 
@@ -891,3 +1055,87 @@ def beam_select(logits, scores, n=None, finished=None, eos=None):
                              -1 if eos is None else int(eos), out_scores.data_ptr(), parents.data_ptr(),
                              tokens.data_ptr(), _addr(out_finished), ws.data_ptr(), n_ws, stream), "kda_beam_select")
     return out_scores, parents, tokens, out_finished
+
+
+def _rows(name, t, dtype, lead, device):
+    """(address, entries of a row, row stride) of a list per row: [*lead, n], rows at one even distance."""
+    if t.dtype != dtype or t.shape[:-1] != lead or t.get_device() != device:
+        raise ValueError("%s must be a %s tensor [%s, n] on cuda:%d (got %s %s on %s)"
+                         % (name, dtype, ", ".join(map(str, lead)), device, t.dtype, tuple(t.shape), t.device))
+    stride, n = t.stride(), t.shape[-1]
+    if lead.numel() <= 1:
+        row = n
+    else:
+        row = stride[-2] if lead[-1] > 1 else stride[0]
+    if (n > 1 and stride[-1] != 1) or (len(lead) == 2 and lead[0] > 1 and stride[0] != lead[1] * row):
+        raise ValueError("the rows of %s must be contiguous and evenly spaced (strides %s)" % (name, stride))
+    return t.data_ptr(), n, row
+
+
+def logits_process(logits, tokens=None, lengths=None, prompt_lengths=None, repetition=None, frequency=None,
+                   presence=None, bias_tokens=None, bias=None, allowed=None, out=None):
+    """Penalties for repeated tokens, biases and a mask on logits, in front of a selection.
+
+    logits: [R, V] or [B, W, V] fp32, bf16 or fp16, rows of V contiguous elements
+    at one even distance. Per row, in this order and in fp32:
+      repetition, fp32 [R]: x > 0 ? x / repetition : x * repetition for the
+        tokens of the history;
+      frequency, presence, fp32 [R]: x - (frequency m + presence) for the tokens
+        that stand m > 0 times in the history past its prompt;
+      bias, fp32 [R, K], of the tokens bias_tokens, int32 [R, K]: x + bias (of
+        several for one token the last);
+      allowed, int32 [R, ceil(V / 32)] or more: bit t & 31 of word t >> 5 is set
+        where token t is allowed; the others become -inf.
+    tokens: the histories, int32 [R, L], of which the first lengths [R] (int32;
+    default L) count and the first prompt_lengths [R] (int32; default 0) are the
+    prompt; entries outside the vocabulary (-1) are skipped. With [B, W, V]
+    logits, [R] stands for [B, W]. Lists and masks may be expanded over all rows.
+    out: a tensor like logits, or logits itself (in place: only what changes is
+    touched); by default a new one, whose rows are padded to 16 bytes. Returns out.
+    """
+    import torch
+    dev = logits.get_device()
+    dtype = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}.get(logits.dtype)
+    if logits.dim() not in (2, 3) or dev < 0 or dtype is None:
+        raise ValueError("logits must be a CUDA tensor [rows, vocab] or [batch, beams, vocab] in fp32, bf16 or fp16, "
+                         "got %s %s on %s" % (logits.dtype, tuple(logits.shape), logits.device))
+    lead, V = logits.shape[:-1], logits.shape[-1]
+    if V < 1:
+        raise ValueError("logits have an empty vocabulary")
+    a = Logits()
+    a.rows, a.vocab, a.dtype = lead.numel(), V, dtype
+    if out is None:
+        step = 4 if dtype == 0 else 8
+        if V % step:
+            out = torch.empty(*lead, -(-V // step) * step, dtype=logits.dtype, device=logits.device)[..., :V]
+        else:
+            out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    elif out.shape != logits.shape:
+        raise ValueError("out must be like logits, %s (got %s)" % (tuple(logits.shape), tuple(out.shape)))
+    a.logits, _, a.row_stride = _rows("logits", logits, logits.dtype, lead, dev)
+    a.out, _, a.out_stride = _rows("out", out, logits.dtype, lead, dev)
+    if tokens is not None:
+        a.tokens, a.max_tokens, a.token_stride = _rows("tokens", tokens, torch.int32, lead, dev)
+        for name, t, dt in (("lengths", lengths, torch.int32), ("prompt_lengths", prompt_lengths, torch.int32),
+                            ("repetition", repetition, torch.float32), ("frequency", frequency, torch.float32),
+                            ("presence", presence, torch.float32)):
+            if t is not None:
+                _need(name, t, dt, lead, dev)
+                setattr(a, name, t.data_ptr())
+    elif not (lengths is prompt_lengths is repetition is frequency is presence is None):
+        raise ValueError("lengths and penalties need tokens")
+    if (bias is None) != (bias_tokens is None):
+        raise ValueError("bias and bias_tokens go together")
+    if bias is not None:
+        a.bias_tokens, a.n_bias, a.bias_stride = _rows("bias_tokens", bias_tokens, torch.int32, lead, dev)
+        a.bias, n, stride = _rows("bias", bias, torch.float32, lead, dev)
+        if n != a.n_bias or (stride != a.bias_stride and a.rows > 1):
+            raise ValueError("bias and bias_tokens must have the same shape and strides (got %s, %s)"
+                             % (bias.stride(), bias_tokens.stride()))
+    if allowed is not None:
+        a.allowed, n, a.allowed_stride = _rows("allowed", allowed, torch.int32, lead, dev)
+        if n < (V + 31) // 32:
+            raise ValueError("allowed must have a bit for each of the %d tokens (got %d words)" % (V, n))
+    L, ctx, stream = _on(dev)
+    _check(L.kda_logits_process(ctx, ctypes.byref(a), stream), "kda_logits_process")
+    return out

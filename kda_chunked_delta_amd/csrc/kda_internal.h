@@ -11,6 +11,7 @@
 #include "gated_delta_launch.h"
 #include "kda.h"
 #include "kda_launch.h"
+#include "linear_attention_launch.h"
 
 namespace kda {
 
@@ -57,6 +58,12 @@ struct kda_plan {
     std::vector<kda::GdUnit> gd_units;  // main launch
     std::vector<kda::GdUnit> gd_pre;    // segments' end states and transfers
     std::vector<kda::GdMerge> gd_merges;
+    // Linear attention plans (kda_plan_linear_attention) have these. off_carry
+    // holds the slots' states, off_b their decays.
+    bool linear = false;
+    std::vector<kda::LaUnit> la_units;  // main launch
+    std::vector<kda::LaUnit> la_pre;    // segments' end states
+    std::vector<kda::LaMerge> la_merges;
     // workspace layout (byte offsets into the arena)
     size_t off_rec = 0, off_b = 0, off_m = 0, off_mlive = 0, off_carry = 0;
     size_t off_spec_states = 0, off_spec_flags = 0, off_gate = 0;

@@ -816,6 +816,7 @@ kda_status kda_prefill_ex_validate(const kda_plan* p, const kda_prefill_opts* op
                                    float scale, const void* s0, const void* sT, const void* out) {
     if (!p) return fail(KDA_ERR_INVALID, "kda_prefill: plan is NULL");
     if (p->gated) return fail(KDA_ERR_INVALID, "kda_prefill: the plan is a gated delta rule plan");
+    if (p->linear) return fail(KDA_ERR_INVALID, "kda_prefill: the plan is a linear attention plan");
     const kda_plan_info& in = p->info;
     const int32_t qk_heads = (opts && opts->qk_heads > 0) ? opts->qk_heads : in.H;
     const bool beta16 = opts && opts->beta_bf16, state16 = opts && opts->state_bf16;

@@ -1,0 +1,474 @@
+// Linear attention with one decay per head on gfx950 (CDNA4): chunked prefill
+// and recurrent decode over a 128 x 128 fp32 state per head:
+//   S_t = exp(g_t) S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
+// with a log-decay g per token and head, or one per head for all tokens.
+//
+// Chunked form. For a chunk of rows r = 0 .. 31 with start state S and G_r the
+// running sum of g inside the chunk:
+//   A = lower((q_r . k_i) exp(G_r - G_i))
+//   O = scale (diag(exp(G)) Q S + A V)
+//   S <- exp(G_31) S + K^T diag(exp(G_31 - G)) V
+// The decay is one number per row: it scales rows of results, and V on its way
+// into the state, never q and k, which go to the matrix instructions as they
+// are in memory. What is computed in fp32 and then multiplied is rounded so:
+//   - diag(exp(G_31 - G)) V becomes a pair hi + lo of bf16 numbers (16 bits of
+//     mantissa), since the state keeps its sum: one bf16 would leave 2^-9 of
+//     each token in an fp32 state, the pair leaves 2^-18;
+//   - A and the copy of S that Q S multiplies become one bf16 each (2^-9): they
+//     only reach the output, which is bf16 itself.
+// All sums are fp32, the running sum of g is fp64 (differences of it are taken).
+#include "chunk_tiles.hpp"
+#include "linear_attention_launch.h"
+
+#include <mutex>
+
+namespace kda {
+namespace {
+
+static_assert(kLaChunk == TILE_ROWS);
+
+// Per-row values of a chunk, fp32 [4][32]: the running log2-decay as hi + lo,
+// exp(G) and exp(G_31 - G).
+constexpr int LS_H = 0, LS_L = 32, LS_GAM = 64, LS_LAST = 96, LS_FLOATS = 128;
+
+// One wavefront: x = the log-decay of row lane & 31.
+__device__ __forceinline__ void row_scan(float x, int lane, float* gs) {
+    const int r = lane & 31;
+    x *= LOG2E;
+    double G = x < LOG2_FLOOR ? LOG2_FLOOR : x;
+#pragma unroll
+    for (int d = 1; d < TILE_ROWS; d <<= 1) {
+        const double y = __shfl_up(G, d, 32);
+        if (r >= d) G += y;
+    }
+    const double all = __shfl(G, 31, 32);
+    const float hi = (float)G;
+    if (lane < TILE_ROWS) {
+        gs[LS_H + r] = hi;
+        gs[LS_L + r] = (float)(G - (double)hi);
+        gs[LS_GAM + r] = exp2_hw(hi);
+        gs[LS_LAST + r] = exp2_hw((float)(all - G));
+    }
+}
+
+// Rows lane & 31 of a tile, the granule of step s of channel tile t: 4t + 2s + h.
+__device__ __forceinline__ u32x4 row32(const uint8_t* tile, int at_row, int t, int s) {
+    return *(const u32x4*)(tile + (at_row ^ ((4 * t + 2 * s) << 4)));
+}
+
+// A of a chunk as the operand of A V: [step s 2][lane 64][8 bf16], lane l
+// holding token l & 31 and the keys 16s + 8 (j >> 2) + 4 (l >> 5) + (j & 3).
+constexpr int A_BYTES = 2048;
+__device__ __forceinline__ void form_a(const uint8_t* Q, const uint8_t* K, const float* gs, float scale, uint8_t* rec,
+                                       int lane) {
+    const int h = lane >> 5, r = lane & 31, at_row = tile_off(r, h);
+    f32x16 x = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int s = 0; s < 2; ++s) x = mfma_32(row32(K, at_row, t, s), row32(Q, at_row, t, s), x);
+    const float hr = gs[LS_H + r], lr = gs[LS_L + r];
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+        const f32x4 hv = *(const f32x4*)(gs + LS_H + 8 * a + 4 * h), lv = *(const f32x4*)(gs + LS_L + 8 * a + 4 * h);
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+            x[4 * a + b] = 8 * a + 4 * h + b <= r ? scale * x[4 * a + b] * pair_decay(hr, lr, hv[b], lv[b]) : 0.f;
+    }
+    u32x4 y[2];
+    pack_rows(x, y);
+    *(u32x4*)(rec + lane * 16) = y[0];
+    *(u32x4*)(rec + 1024 + lane * 16) = y[1];
+}
+
+// Prefill: one workgroup per (unit, head), in a software pipeline with one
+// barrier per chunk. In interval i
+//   wavefronts 4 .. 7 advance the state over chunk i (32 value columns each)
+//     and form its output;
+//   wavefronts 0 .. 3 issue the direct-to-LDS loads of q, k and v of chunk
+//     i + AHEAD (8 rows each), which stay in flight for AHEAD - 2 intervals;
+//     0 forms A of chunk i + 1, 3 the row values of chunk i + 2 and loads the
+//     log-decays of chunk i + AHEAD + 1.
+// Ring slots: the tiles AHEAD + 1 chunks, A 2, the row values 3.
+constexpr int AHEAD = 5;
+constexpr int N_TILE = AHEAD + 1, N_A = 2, N_GS = 3, N_G = AHEAD + 2;
+constexpr int LEAD = AHEAD + 1;  // intervals before chunk 0
+template <bool OUT>
+struct Lds {
+    alignas(16) uint8_t k[N_TILE][TILE_BYTES];
+    alignas(16) uint8_t v[N_TILE][TILE_BYTES];
+    alignas(16) uint8_t q[OUT ? N_TILE : 1][OUT ? TILE_BYTES : 16];
+    alignas(16) uint8_t a[OUT ? N_A : 1][OUT ? A_BYTES : 16];
+    alignas(16) float gs[N_GS][LS_FLOATS];
+    alignas(16) float g[N_G][64];  // the loads write 64 lanes; rows past the chunk hold zeros
+};
+
+// What a workgroup works on (uniform).
+struct Work {
+    const uint8_t *q, *k, *v;  // the unit's first rows of its head
+    const float* g;
+    uint32_t st_qk, st_v, st_g;  // bytes from row to row
+    int n_tok, n_chunks;
+    float scale;
+};
+
+template <int ROLE, bool OUT>
+__device__ __forceinline__ void produce(const Work& w, Lds<OUT>& lds, int lane) {
+    Ring<N_TILE> tile;
+    Ring<N_A> ra;
+    Ring<N_GS> gs;
+    Ring<N_G> rg;
+    auto load = [&](const uint8_t* base, uint32_t stride, int c, int rows, uint8_t* to) __attribute__((always_inline)) {
+        const auto rsrc = chunk_rsrc(base + (size_t)(c < 0 ? 0 : c) * TILE_ROWS * stride, (uint32_t)rows * stride);
+        load_rows(rsrc, stride, 2 * ROLE, lane, to);
+        load_rows(rsrc, stride, 2 * ROLE + 1, lane, to);
+    };
+    // ring position j is chunk i + j
+    for (int i = -LEAD; i < w.n_chunks; ++i) {
+        const int c = i + AHEAD, rows = rows_of_chunk(w.n_tok, c);
+        load(w.k, w.st_qk, c, rows, lds.k[tile.at[AHEAD]]);
+        load(w.v, w.st_v, c, rows, lds.v[tile.at[AHEAD]]);
+        if constexpr (OUT) load(w.q, w.st_qk, c, rows, lds.q[tile.at[AHEAD]]);
+        if constexpr (ROLE == 3) {  // a fixed decay has st_g = 0
+            const int left = rows_of_chunk(w.n_tok, c + 1);
+            const uint32_t range = __builtin_amdgcn_readfirstlane(left ? (uint32_t)(left - 1) * w.st_g + 4 : 0u);
+            const auto rsrc = chunk_rsrc((const uint8_t*)w.g + (size_t)(c + 1) * TILE_ROWS * w.st_g, range);
+            const uint32_t off = lane < left ? (uint32_t)lane * w.st_g : 0x7ffffffcu;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rsrc, (__attribute__((address_space(3))) void*)lds.g[rg.at[AHEAD + 1]], 4, (int)off, 0, 0, 0);
+            if (i + 2 >= 0 && i + 2 < w.n_chunks) row_scan(lds.g[rg.at[2]][lane & 31], lane, lds.gs[gs.at[2]]);
+        }
+        if constexpr (ROLE == 0 && OUT)
+            if (i + 1 >= 0 && i + 1 < w.n_chunks)
+                form_a(lds.q[tile.at[1]], lds.k[tile.at[1]], lds.gs[gs.at[1]], w.scale, lds.a[ra.at[1]], lane);
+        // the loads of the last AHEAD - 2 intervals are still on their way; those before have landed
+        constexpr int ISSUED = (OUT ? 6 : 4) + (ROLE == 3 ? 1 : 0);
+        asm volatile("s_waitcnt vmcnt(%0)" ::"n"(ISSUED * (AHEAD - 2)) : "memory");
+        lds_barrier();
+        tile.next();
+        ra.next();
+        gs.next();
+        rg.next();
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS outlives the workgroup
+}
+
+template <bool OUT>
+__global__ __launch_bounds__(kLaThreads) void la_prefill(LaArgs a) {
+    extern __shared__ __align__(16) uint8_t lds_raw[];
+    Lds<OUT>& lds = *(Lds<OUT>*)lds_raw;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int hd = blockIdx.x % a.H;
+    const LaUnit un = a.units[blockIdx.x / a.H];
+    // the unit's tokens, clamped into the sequence and the inputs
+    int64_t beg = a.cu[un.seq], end = a.cu[un.seq + 1];
+    end = end > a.Tt ? a.Tt : end;
+    beg = (beg < 0 ? 0 : beg) + un.tok0;
+    end = end < beg + un.n_tok ? end : beg + un.n_tok;
+    const int n_tok = __builtin_amdgcn_readfirstlane(end > beg ? (int)(end - beg) : 0);
+    const int n_chunks = (int)(((int64_t)n_tok + TILE_ROWS - 1) / TILE_ROWS);
+    const uint32_t st_v = (uint32_t)a.H * (D * 2);
+
+    if (wave < 4) {
+        Work w;
+        const int64_t row = beg * a.H + hd, row_qk = (beg * a.Hk + hd / a.group) * (D * 2);
+        w.q = (const uint8_t*)a.q + row_qk;
+        w.k = (const uint8_t*)a.k + row_qk;
+        w.v = (const uint8_t*)a.v + row * (D * 2);
+        w.g = a.g + (a.g_fixed ? hd : row);
+        w.st_qk = (uint32_t)a.Hk * (D * 2);
+        w.st_v = st_v;
+        w.st_g = a.g_fixed ? 0u : (uint32_t)a.H * 4;
+        w.n_tok = n_tok;
+        w.n_chunks = n_chunks;
+        w.scale = a.scale;
+        if (wave == 0) produce<0, OUT>(w, lds, lane);
+        else if (wave == 1) produce<1, OUT>(w, lds, lane);
+        else if (wave == 2) produce<2, OUT>(w, lds, lane);
+        else produce<3, OUT>(w, lds, lane);
+        return;
+    }
+
+    // wavefronts 4 .. 7: the state, 32 value columns each
+    const int col0 = 32 * (wave & 3);
+    const int h = lane >> 5, odd = (lane >> 4) & 1, r = (lane >> 2) & 3, c = lane & 3;
+    f32x16 S[4];
+    // the element of the 128 x 128 state that element 4a + b of tile t is on this lane
+    const int at0 = 8 * h * D + col0 + value_col(lane & 31);
+    auto each = [&](auto f) __attribute__((always_inline)) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                S[t][i] = f(at0 + (32 * t + 16 * (i >> 3) + (i & 7)) * D, S[t][i]);
+    };
+    const int64_t own = ((int64_t)un.seq * a.H + hd) * (D * D);
+    if (un.in >= 0) {
+        const float* p = a.slots + ((int64_t)un.in * a.H + hd) * (D * D);
+        each([&](int at, float) { return p[at]; });
+    } else if (un.in == LA_INITIAL && a.s0) {
+        if (a.state_bf16) {
+            const uint16_t* p = (const uint16_t*)a.s0 + own;
+            each([&](int at, float) { return __uint_as_float((uint32_t)p[at] << 16); });
+        } else {
+            const float* p = (const float*)a.s0 + own;
+            each([&](int at, float) { return p[at]; });
+        }
+    } else {
+        each([&](int, float) { return 0.f; });
+    }
+    for (int i = -LEAD; i < 0; ++i) lds_barrier();
+    uint8_t* ob = (uint8_t*)a.out + (beg * a.H + hd) * (D * 2);
+    Ring<N_TILE> tile;
+    Ring<N_A> ra;
+    Ring<N_GS> gs;
+#pragma unroll
+    for (int i = 0; i < LEAD; ++i) {
+        tile.next();
+        ra.next();
+        gs.next();
+    }
+    float all = 1.f;  // the decay over the unit's tokens
+    const int at_row = opaque(tile_off(lane & 31, h));
+    // K^T: lane row l & 31 of tile t is channel 32t + 16 odd + 8 (i >> 2 & 1) + 4 (i >> 3) + (i & 3), i = l & 15
+    const int at_col0 = opaque(tile_off(4 * h + r, 2 * odd + (c & 1)) + 8 * (c >> 1));
+    const int at_col1 = opaque(tile_off(8 + 4 * h + r, 2 * odd + (c & 1)) + 8 * (c >> 1));
+    for (int i = 0; i < n_chunks; ++i) {
+        const uint8_t *K = lds.k[tile.at[0]], *V = lds.v[tile.at[0]];
+        const float* row = lds.gs[gs.at[0]];
+        // V: rows 16s + 8 (j >> 2) + 4h + (j & 3) of the lane's column value_col(l & 31)
+        u32x4 vw[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const u32x2 x = lds_load_tr16(V + tile_off(16 * s + 4 * h + r, (col0 >> 3) + 2 * (c & 1) + odd) + 8 * (c >> 1));
+            const u32x2 y =
+                lds_load_tr16(V + tile_off(16 * s + 8 + 4 * h + r, (col0 >> 3) + 2 * (c & 1) + odd) + 8 * (c >> 1));
+            vw[s] = u32x4{x.x, x.y, y.x, y.y};
+        }
+        const float gc = row[LS_GAM + 31];
+        if constexpr (OUT) {
+            const uint8_t* Q = lds.q[tile.at[0]];
+            f32x16 o = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                u32x4 sb[2];
+                pack_rows(S[t], sb);
+#pragma unroll
+                for (int s = 0; s < 2; ++s) o = mfma_32(sb[s], row32(Q, at_row, t, s), o);
+            }
+            const uint8_t* rec = lds.a[ra.at[0]];
+            o = (a.scale * row[LS_GAM + (lane & 31)]) * o;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) o = mfma_32(vw[s], *(const u32x4*)(rec + s * 1024 + lane * 16), o);
+            // token l & 31, element 4a + b being value column 16h + 4a + b
+            const auto rsrc = chunk_rsrc(ob + (size_t)i * TILE_ROWS * st_v, (uint32_t)rows_of_chunk(n_tok, i) * st_v);
+            const int at = (int)((lane & 31) * st_v) + (col0 + 16 * h) * 2;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const u32x2 x = pack4(quarter(o, 2 * j)), y = pack4(quarter(o, 2 * j + 1));
+                __builtin_amdgcn_raw_buffer_store_b128(u32x4{x.x, x.y, y.x, y.y}, rsrc, at + 16 * j, 0, 0);
+            }
+        }
+        // diag(exp(G_31 - G)) V as hi + lo
+        u32x4 wh[2], wl[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            HiLo x[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const f32x4 last = *(const f32x4*)(row + LS_LAST + 16 * s + 8 * j + 4 * h);
+                const uint32_t p = vw[s][2 * j], q = vw[s][2 * j + 1];
+                x[j] = split4(f32x4{last[0] * bf16_lo(p), last[1] * bf16_hi(p), last[2] * bf16_lo(q), last[3] * bf16_hi(q)});
+            }
+            wh[s] = u32x4{x[0].h.x, x[0].h.y, x[1].h.x, x[1].h.y};
+            wl[s] = u32x4{x[0].l.x, x[0].l.y, x[1].l.x, x[1].l.y};
+        }
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            S[t] = gc * S[t];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const u32x2 k0 = lds_load_tr16(K + (at_col0 ^ (4 * t << 4)) + 4096 * s);
+                const u32x2 k1 = lds_load_tr16(K + (at_col1 ^ (4 * t << 4)) + 4096 * s);
+                const u32x4 kt = {k0.x, k0.y, k1.x, k1.y};
+                S[t] = mfma_32(kt, wh[s], S[t]);
+                S[t] = mfma_32(kt, wl[s], S[t]);
+            }
+        }
+        if constexpr (!OUT) all *= gc;
+        lds_barrier();
+        tile.next();
+        ra.next();
+        gs.next();
+    }
+    if (un.out >= 0) {
+        float* p = a.slots + ((int64_t)un.out * a.H + hd) * (D * D);
+        each([&](int at, float s) { return p[at] = s; });
+        if (threadIdx.x == kLaThreads - 1) a.decays[(int64_t)un.out * a.H + hd] = all;
+    } else if (un.out == LA_FINAL && a.sT) {
+        if (a.state_bf16) {
+            uint16_t* p = (uint16_t*)a.sT + own;
+            each([&](int at, float s) {
+                p[at] = (uint16_t)pack_bf16(s, 0.f);
+                return s;
+            });
+        } else {
+            float* p = (float*)a.sT + own;
+            each([&](int at, float s) { return p[at] = s; });
+        }
+    }
+}
+
+// The states between segments: slot 0 gets the initial state, and slot s + 1,
+// which holds the end state of segment s from zero, is added the decayed slot s.
+// One thread per four elements of a state; the loads of DEEP segments are in
+// flight together.
+constexpr int DEEP = 8;
+static_assert(kLaMergeTiles * kLaMergeThreads * 4 == D * D);
+__global__ __launch_bounds__(kLaMergeThreads) void la_merge(LaMergeArgs a) {
+    const int tile = blockIdx.x % kLaMergeTiles, ih = blockIdx.x / kLaMergeTiles, hd = ih % a.H;
+    const LaMerge it = a.items[ih / a.H];
+    const int at = (tile * kLaMergeThreads + threadIdx.x) * 4;
+    const int64_t own = ((int64_t)it.seq * a.H + hd) * (D * D) + at;
+    f32x4 c = {0.f, 0.f, 0.f, 0.f};
+    if (a.s0 && a.state_bf16) {
+        const u32x2 x = *(const u32x2*)((const uint16_t*)a.s0 + own);
+        c = f32x4{bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y)};
+    } else if (a.s0) {
+        c = *(const f32x4*)((const float*)a.s0 + own);
+    }
+    auto slot = [&](int s) { return ((int64_t)(it.slot0 + s) * a.H + hd); };
+    *(f32x4*)(a.slots + slot(0) * (D * D) + at) = c;
+    for (int s0 = 1; s0 < it.n; s0 += DEEP) {
+        f32x4 b[DEEP];
+        float gam[DEEP];
+#pragma unroll
+        for (int j = 0; j < DEEP; ++j)
+            if (s0 + j < it.n) {
+                b[j] = *(const f32x4*)(a.slots + slot(s0 + j) * (D * D) + at);
+                gam[j] = a.decays[slot(s0 + j)];
+            }
+#pragma unroll
+        for (int j = 0; j < DEEP; ++j)
+            if (s0 + j < it.n) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) c[e] = __builtin_fmaf(gam[j], c[e], b[j][e]);
+                *(f32x4*)(a.slots + slot(s0 + j) * (D * D) + at) = c;
+            }
+    }
+}
+
+// Decode. With S the state before a token and gam = exp(g), for value column j:
+//   o_j = scale (gam sum_r q_r S_rj + (q . k) v_j),   S'_rj = gam S_rj + k_r v_j
+// One wavefront per (sequence, head, 32-column tile) keeps its part of the
+// state in registers over all T tokens: lane (rs, cg) = (lane >> 3, lane & 7)
+// owns rows 16rs .. + 15 of columns 4cg .. + 3, so a load instruction covers
+// eight whole 128-byte lines, the sums need three lane exchanges and the
+// kernel needs neither LDS nor a barrier.
+static_assert(kLaDecodeThreads == 64 * 4);  // a wavefront per 32-column tile
+
+template <bool NT>
+__global__ __launch_bounds__(kLaDecodeThreads) void la_decode(LaDecodeArgs a) {
+    const int lane = threadIdx.x & 63, tile = threadIdx.x >> 6;
+    const int64_t nh = blockIdx.x;
+    const int64_t n = nh / a.H;
+    const int hd = (int)(nh % a.H), hq = hd / a.group;
+    const int rs = lane >> 3, col = 32 * tile + 4 * (lane & 7);
+    const int64_t slot = a.slots ? (int64_t)a.slots[n] : n;
+    if (slot < 0 || slot >= a.n_slots) {
+        for (int t = rs; t < a.T; t += 8) *(uint2*)(a.out + ((n * a.T + t) * a.H + hd) * D + col) = uint2{0u, 0u};
+        return;
+    }
+    f32x4* st = (f32x4*)(a.state + (slot * a.H + hd) * (D * D) + (16 * rs) * D + col);
+    f32x4 s[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        if constexpr (NT) s[i] = __builtin_nontemporal_load(st + i * (D / 4));
+        else s[i] = st[i * (D / 4)];
+    }
+    for (int t = 0; t < a.T; ++t) {
+        const int64_t row = (n * a.T + t) * a.H + hd, rq = (n * a.T + t) * a.Hk + hq;
+        const u32x4* kp = (const u32x4*)(a.k + rq * D + 16 * rs);
+        const u32x4* qp = (const u32x4*)(a.q + rq * D + 16 * rs);
+        const u32x4 k2[2] = {kp[0], kp[1]}, q2[2] = {qp[0], qp[1]};
+        const u32x2 vb = *(const u32x2*)(a.v + row * D + col);
+        const float gam = exp2_hw(a.g[a.g_fixed ? hd : row] * LOG2E);
+        float k[16], q[16], qk = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            k[2 * i] = bf16_lo(k2[i >> 2][i & 3]);
+            k[2 * i + 1] = bf16_hi(k2[i >> 2][i & 3]);
+            q[2 * i] = bf16_lo(q2[i >> 2][i & 3]);
+            q[2 * i + 1] = bf16_hi(q2[i >> 2][i & 3]);
+        }
+        const f32x4 v = {bf16_lo(vb.x), bf16_hi(vb.x), bf16_lo(vb.y), bf16_hi(vb.y)};
+        f32x4 sb = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            qk = __builtin_fmaf(q[i], k[i], qk);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                sb[j] = __builtin_fmaf(q[i], s[i][j], sb[j]);
+                s[i][j] = __builtin_fmaf(gam, s[i][j], k[i] * v[j]);
+            }
+        }
+#pragma unroll
+        for (int d = 8; d < 64; d <<= 1) {
+            qk += __shfl_xor(qk, d, 64);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sb[j] += __shfl_xor(sb[j], d, 64);
+        }
+        f32x4 o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = a.scale * __builtin_fmaf(gam, sb[j], qk * v[j]);
+        if (rs == 0) *(u32x2*)(a.out + row * D + col) = pack4(o);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        if constexpr (NT) __builtin_nontemporal_store(s[i], st + i * (D / 4));
+        else st[i * (D / 4)] = s[i];
+    }
+}
+
+template <bool OUT>
+hipError_t run_la_prefill(const LaArgs& a, hipStream_t s) {
+    // more LDS than the default limit, allowed once per device and process
+    static std::mutex mu;
+    static uint64_t done[4] = {0, 0, 0, 0};
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        if (dev >= 256 || !(done[dev >> 6] >> (dev & 63) & 1)) {
+            e = hipFuncSetAttribute((const void*)la_prefill<OUT>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)sizeof(Lds<OUT>));
+            if (e != hipSuccess) return e;
+            if (dev < 256) done[dev >> 6] |= 1ull << (dev & 63);
+        }
+    }
+    hipLaunchKernelGGL((la_prefill<OUT>), dim3((unsigned)(a.n_units * a.H)), dim3(kLaThreads), sizeof(Lds<OUT>), s, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_la_prefill(const LaArgs& a, bool with_out, hipStream_t s) {
+    if (a.n_units == 0) return hipSuccess;
+    return with_out ? run_la_prefill<true>(a, s) : run_la_prefill<false>(a, s);
+}
+
+hipError_t launch_la_merge(const LaMergeArgs& a, hipStream_t s) {
+    hipLaunchKernelGGL(la_merge, dim3((unsigned)(a.n_items * a.H * kLaMergeTiles)), dim3(kLaMergeThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_la_decode(const LaDecodeArgs& a, hipStream_t s) {
+    const dim3 grid((unsigned)(a.n_seqs * a.H)), block(kLaDecodeThreads);
+    const bool nt = (size_t)a.n_seqs * a.H * (D * D * 4) > ((size_t)128 << 20);
+    if (nt) hipLaunchKernelGGL(la_decode<true>, grid, block, 0, s, a);
+    else hipLaunchKernelGGL(la_decode<false>, grid, block, 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace kda
