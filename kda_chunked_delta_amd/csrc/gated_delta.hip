@@ -197,30 +197,6 @@ __device__ __forceinline__ void qk_tiles(const uint8_t* Q, const uint8_t* K, con
         }
 }
 
-// The rest x - hi of a tile is formed by the matrix unit, as x + (-1) hi with
-// the operand of -1 in minus_one[s]. It is exact, and two matrix instructions
-// stand in for 32 vector ones, which bound the chain otherwise.
-struct MinusOne {
-    u32x4 s[2];
-};
-__device__ __forceinline__ MinusOne minus_one(int lane) {
-    const int row = lane & 31, h = lane >> 5;
-    MinusOne m;
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const int r = row - (16 * s + 8 * (w >> 1) + 4 * h + 2 * (w & 1));  // 0: the low half, 1: the high
-            m.s[s][w] = r == 0 ? 0x0000bf80u : r == 1 ? 0xbf800000u : 0u;
-        }
-    return m;
-}
-__device__ __forceinline__ f32x16 rest_of(const f32x16& x, const u32x4 (&hi)[2], const MinusOne& m) {
-    return mfma_32(m.s[1], hi[1], mfma_32(m.s[0], hi[0], x));
-}
-
-// Nothing is scheduled across sched_fence.
-__device__ __forceinline__ void sched_fence() { __builtin_amdgcn_sched_barrier(0); }
 // Fixes the place of what forms or uses x among the other pins.
 template <class T>
 __device__ __forceinline__ void pin(T& x) { asm volatile("" : "+v"(x)); }

@@ -11,9 +11,9 @@
 // The decay is one number per row: it scales rows of results, and V on its way
 // into the state, never q and k, which go to the matrix instructions as they
 // are in memory. What is computed in fp32 and then multiplied is rounded so:
-//   - diag(exp(G_31 - G)) V becomes a pair hi + lo of bf16 numbers (16 bits of
-//     mantissa), since the state keeps its sum: one bf16 would leave 2^-9 of
-//     each token in an fp32 state, the pair leaves 2^-18;
+//   - diag(exp(G_31 - G)) V becomes the sum of three bf16 numbers, all 24 bits of
+//     its mantissa, since the state keeps its sum: one bf16 would leave 2^-9 of
+//     each token in an fp32 state, two 2^-18;
 //   - A and the copy of S that Q S multiplies become one bf16 each (2^-9): they
 //     only reach the output, which is bf16 itself.
 // All sums are fp32, the running sum of g is fp64 (differences of it are taken).
@@ -58,27 +58,63 @@ __device__ __forceinline__ u32x4 row32(const uint8_t* tile, int at_row, int t, i
 
 // A of a chunk as the operand of A V: [step s 2][lane 64][8 bf16], lane l
 // holding token l & 31 and the keys 16s + 8 (j >> 2) + 4 (l >> 5) + (j & 3).
+// One wavefront forms the 16 x 16 tile of tokens 16 rt .. and keys 16 ct .. :
+// lane (gg, m) has token 16 rt + m and keys 16 ct + 4 gg + b, half a lane's
+// entry. Tile (0, 1) is zero; it is cleared once and never written.
 constexpr int A_BYTES = 2048;
+__device__ __forceinline__ uint8_t* a_tile(uint8_t* rec, int rt, int ct, int lane) {
+    const int gg = lane >> 4, m = lane & 15;
+    return rec + ct * 1024 + (32 * (gg & 1) + 16 * rt + m) * 16 + 8 * (gg >> 1);
+}
+__device__ __forceinline__ u32x4 row16(const uint8_t* tile, int row0, int p, int lane) {
+    return *(const u32x4*)(tile + tile_off(row0 + (lane & 15), 4 * p + (lane >> 4)));
+}
+template <int RT, int CT>
 __device__ __forceinline__ void form_a(const uint8_t* Q, const uint8_t* K, const float* gs, float scale, uint8_t* rec,
                                        int lane) {
-    const int h = lane >> 5, r = lane & 31, at_row = tile_off(r, h);
-    f32x16 x = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const int gg = lane >> 4, m = lane & 15;
+    f32x4 x = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+    for (int p = 0; p < 4; ++p) x = mfma_k32(row16(K, 16 * CT, p, lane), row16(Q, 16 * RT, p, lane), x);
+    const f32x4 hv = *(const f32x4*)(gs + LS_H + 16 * CT + 4 * gg), lv = *(const f32x4*)(gs + LS_L + 16 * CT + 4 * gg);
+    const float hm = gs[LS_H + 16 * RT + m], lm = gs[LS_L + 16 * RT + m];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) x = mfma_32(row32(K, at_row, t, s), row32(Q, at_row, t, s), x);
-    const float hr = gs[LS_H + r], lr = gs[LS_L + r];
-#pragma unroll
-    for (int a = 0; a < 4; ++a) {
-        const f32x4 hv = *(const f32x4*)(gs + LS_H + 8 * a + 4 * h), lv = *(const f32x4*)(gs + LS_L + 8 * a + 4 * h);
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-            x[4 * a + b] = 8 * a + 4 * h + b <= r ? scale * x[4 * a + b] * pair_decay(hr, lr, hv[b], lv[b]) : 0.f;
+    for (int b = 0; b < 4; ++b)
+        x[b] = CT < RT || 4 * gg + b <= m ? scale * x[b] * pair_decay(hm, lm, hv[b], lv[b]) : 0.f;
+    *(u32x2*)a_tile(rec, RT, CT, lane) = pack4(x);
+}
+
+// A wait for the wavefront's LDS traffic that the compiler counts: it then knows
+// that loads issued before have come, and does not wait for later ones instead.
+__device__ __forceinline__ void counted_wait() {
+    sched_fence();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0)
+    asm volatile("" ::: "memory");
+    sched_fence();
+}
+
+// Sixteen weighted values of a lane as three bf16 operands a + b + c that make
+// them up (8 bits of mantissa each).
+struct Split3 {
+    u32x4 a[2], b[2], c[2];
+};
+// Their formation in parts, to go beside other products. Values 2n and 2n + 1 of
+// the lane's 16, first weighted (x), then what is left of them.
+template <int N>
+__device__ __forceinline__ void weigh(f32x16& x, const u32x4 (&v)[2], const f32x4 (&w)[4], u32x4 (&to)[2]) {
+    const uint32_t p = v[N >> 2][N & 3];
+    x[2 * N] = w[N >> 1][2 * (N & 1)] * bf16_lo(p);
+    x[2 * N + 1] = w[N >> 1][2 * (N & 1) + 1] * bf16_hi(p);
+    to[N >> 2][N & 3] = pack_bf16(x[2 * N], x[2 * N + 1]);
+}
+
+template <int N, class F>
+__device__ __forceinline__ void unrolled(F f) {
+    if constexpr (N > 0) {
+        unrolled<N - 1>(f);
+        f(std::integral_constant<int, N - 1>{});
     }
-    u32x4 y[2];
-    pack_rows(x, y);
-    *(u32x4*)(rec + lane * 16) = y[0];
-    *(u32x4*)(rec + 1024 + lane * 16) = y[1];
 }
 
 // Prefill: one workgroup per (unit, head), in a software pipeline with one
@@ -87,8 +123,8 @@ __device__ __forceinline__ void form_a(const uint8_t* Q, const uint8_t* K, const
 //     and form its output;
 //   wavefronts 0 .. 3 issue the direct-to-LDS loads of q, k and v of chunk
 //     i + AHEAD (8 rows each), which stay in flight for AHEAD - 2 intervals;
-//     0 forms A of chunk i + 1, 3 the row values of chunk i + 2 and loads the
-//     log-decays of chunk i + AHEAD + 1.
+//     0, 1 and 2 form a tile of A of chunk i + 1 each, 3 the row values of chunk
+//     i + 2, and loads the log-decays of chunk i + AHEAD + 1.
 // Ring slots: the tiles AHEAD + 1 chunks, A 2, the row values 3.
 constexpr int AHEAD = 5;
 constexpr int N_TILE = AHEAD + 1, N_A = 2, N_GS = 3, N_G = AHEAD + 2;
@@ -138,9 +174,10 @@ __device__ __forceinline__ void produce(const Work& w, Lds<OUT>& lds, int lane) 
                 rsrc, (__attribute__((address_space(3))) void*)lds.g[rg.at[AHEAD + 1]], 4, (int)off, 0, 0, 0);
             if (i + 2 >= 0 && i + 2 < w.n_chunks) row_scan(lds.g[rg.at[2]][lane & 31], lane, lds.gs[gs.at[2]]);
         }
-        if constexpr (ROLE == 0 && OUT)
+        if constexpr (ROLE < 3 && OUT)  // tiles (0, 0), (1, 0) and (1, 1)
             if (i + 1 >= 0 && i + 1 < w.n_chunks)
-                form_a(lds.q[tile.at[1]], lds.k[tile.at[1]], lds.gs[gs.at[1]], w.scale, lds.a[ra.at[1]], lane);
+                form_a<(ROLE > 0), (ROLE > 1)>(lds.q[tile.at[1]], lds.k[tile.at[1]], lds.gs[gs.at[1]], w.scale,
+                                               lds.a[ra.at[1]], lane);
         // the loads of the last AHEAD - 2 intervals are still on their way; those before have landed
         constexpr int ISSUED = (OUT ? 6 : 4) + (ROLE == 3 ? 1 : 0);
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"(ISSUED * (AHEAD - 2)) : "memory");
@@ -189,7 +226,9 @@ __global__ __launch_bounds__(kLaThreads) void la_prefill(LaArgs a) {
         return;
     }
 
-    // wavefronts 4 .. 7: the state, 32 value columns each
+    // wavefronts 4 .. 7: the state, 32 value columns each. Each shares its SIMD
+    // with an operand wavefront, whose work is to fall beside the products.
+    __builtin_amdgcn_s_setprio(2);
     const int col0 = 32 * (wave & 3);
     const int h = lane >> 5, odd = (lane >> 4) & 1, r = (lane >> 2) & 3, c = lane & 3;
     f32x16 S[4];
@@ -217,6 +256,8 @@ __global__ __launch_bounds__(kLaThreads) void la_prefill(LaArgs a) {
     } else {
         each([&](int, float) { return 0.f; });
     }
+    if constexpr (OUT)
+        if (wave < 4 + N_A) *(u32x2*)a_tile(lds.a[wave - 4], 0, 1, lane) = u32x2{0, 0};
     for (int i = -LEAD; i < 0; ++i) lds_barrier();
     uint8_t* ob = (uint8_t*)a.out + (beg * a.H + hd) * (D * 2);
     Ring<N_TILE> tile;
@@ -233,70 +274,127 @@ __global__ __launch_bounds__(kLaThreads) void la_prefill(LaArgs a) {
     // K^T: lane row l & 31 of tile t is channel 32t + 16 odd + 8 (i >> 2 & 1) + 4 (i >> 3) + (i & 3), i = l & 15
     const int at_col0 = opaque(tile_off(4 * h + r, 2 * odd + (c & 1)) + 8 * (c >> 1));
     const int at_col1 = opaque(tile_off(8 + 4 * h + r, 2 * odd + (c & 1)) + 8 * (c >> 1));
+    const int at_v0 = opaque(tile_off(4 * h + r, (col0 >> 3) + 2 * (c & 1) + odd) + 8 * (c >> 1));
+    const int at_v1 = opaque(tile_off(8 + 4 * h + r, (col0 >> 3) + 2 * (c & 1) + odd) + 8 * (c >> 1));
+    auto columns = [&](const uint8_t* tile, int at0, int at1) __attribute__((always_inline)) {
+        const u32x2 x = lds_load_tr16(tile + at0), y = lds_load_tr16(tile + at1);
+        return u32x4{x.x, x.y, y.x, y.y};
+    };
+    // While one chunk is worked on, Q, V and the first half of K^T of the next are read (they have landed an interval
+    // before) and its V is weighted: LDS and VALU work beside the products. V: rows 16s + 8 (j >> 2) + 4h + (j & 3) of
+    // the lane's column value_col(l & 31).
+    u32x4 qf[4][2], kt[4][2], vw[2];
+    f32x4 last[4];
+    Split3 w;
+    auto fetch_v = [&](int slot, const float* row) __attribute__((always_inline)) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) vw[s] = columns(lds.v[slot] + 4096 * s, at_v0, at_v1);
+#pragma unroll
+        for (int a = 0; a < 4; ++a) last[a] = *(const f32x4*)(row + LS_LAST + 8 * a + 4 * h);
+    };
+    float gam_all, gam_row = 0.f;
+    auto fetch_gam = [&](const float* row) __attribute__((always_inline)) {
+        gam_all = row[LS_GAM + 31];
+        if constexpr (OUT) gam_row = a.scale * row[LS_GAM + (lane & 31)];
+    };
+    auto fetch_q = [&](int slot, int t, int s) __attribute__((always_inline)) {
+        if constexpr (OUT) qf[t][s] = row32(lds.q[slot], at_row, t, s);
+    };
+    auto fetch_k = [&](int slot, int t, int s) __attribute__((always_inline)) {
+        kt[t][s] = columns(lds.k[slot] + 4096 * s, at_col0 ^ (4 * t << 4), at_col1 ^ (4 * t << 4));
+    };
+    fetch_gam(lds.gs[gs.at[0]]);
+    fetch_v(tile.at[0], lds.gs[gs.at[0]]);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        fetch_q(tile.at[0], t, 0);
+        fetch_q(tile.at[0], t, 1);
+        fetch_k(tile.at[0], t, 0);
+    }
+    const MinusOne neg = minus_one(lane);
+    {
+        f32x16 x;
+        unrolled<8>([&](auto n) __attribute__((always_inline)) { weigh<n()>(x, vw, last, w.a); });
+        x = rest_of(x, w.a, neg);
+        pack_rows(x, w.b);
+        x = rest_of(x, w.b, neg);
+        pack_rows(x, w.c);
+    }
+    counted_wait();
     for (int i = 0; i < n_chunks; ++i) {
-        const uint8_t *K = lds.k[tile.at[0]], *V = lds.v[tile.at[0]];
-        const float* row = lds.gs[gs.at[0]];
-        // V: rows 16s + 8 (j >> 2) + 4h + (j & 3) of the lane's column value_col(l & 31)
-        u32x4 vw[2];
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const u32x2 x = lds_load_tr16(V + tile_off(16 * s + 4 * h + r, (col0 >> 3) + 2 * (c & 1) + odd) + 8 * (c >> 1));
-            const u32x2 y =
-                lds_load_tr16(V + tile_off(16 * s + 8 + 4 * h + r, (col0 >> 3) + 2 * (c & 1) + odd) + 8 * (c >> 1));
-            vw[s] = u32x4{x.x, x.y, y.x, y.y};
-        }
-        const float gc = row[LS_GAM + 31];
-        if constexpr (OUT) {
-            const uint8_t* Q = lds.q[tile.at[0]];
-            f32x16 o = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                u32x4 sb[2];
-                pack_rows(S[t], sb);
-#pragma unroll
-                for (int s = 0; s < 2; ++s) o = mfma_32(sb[s], row32(Q, at_row, t, s), o);
-            }
-            const uint8_t* rec = lds.a[ra.at[0]];
-            o = (a.scale * row[LS_GAM + (lane & 31)]) * o;
-#pragma unroll
-            for (int s = 0; s < 2; ++s) o = mfma_32(vw[s], *(const u32x4*)(rec + s * 1024 + lane * 16), o);
-            // token l & 31, element 4a + b being value column 16h + 4a + b
-            const auto rsrc = chunk_rsrc(ob + (size_t)i * TILE_ROWS * st_v, (uint32_t)rows_of_chunk(n_tok, i) * st_v);
-            const int at = (int)((lane & 31) * st_v) + (col0 + 16 * h) * 2;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const u32x2 x = pack4(quarter(o, 2 * j)), y = pack4(quarter(o, 2 * j + 1));
-                __builtin_amdgcn_raw_buffer_store_b128(u32x4{x.x, x.y, y.x, y.y}, rsrc, at + 16 * j, 0, 0);
-            }
-        }
-        // diag(exp(G_31 - G)) V as hi + lo
-        u32x4 wh[2], wl[2];
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            HiLo x[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const f32x4 last = *(const f32x4*)(row + LS_LAST + 16 * s + 8 * j + 4 * h);
-                const uint32_t p = vw[s][2 * j], q = vw[s][2 * j + 1];
-                x[j] = split4(f32x4{last[0] * bf16_lo(p), last[1] * bf16_hi(p), last[2] * bf16_lo(q), last[3] * bf16_hi(q)});
-            }
-            wh[s] = u32x4{x[0].h.x, x[0].h.y, x[1].h.x, x[1].h.y};
-            wl[s] = u32x4{x[0].l.x, x[0].l.y, x[1].l.x, x[1].l.y};
-        }
+        const float gc = gam_all, gm = gam_row;
+        const u32x4 v0 = vw[0], v1 = vw[1];
+        u32x4 ab[2], sb[2];
+        f32x16 o = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if constexpr (OUT) pack_rows(S[0], sb);
+        sched_fence();
+        // o = S Q, then S decays. A product of the matrix unit takes 32 cycles and leaves room for some five vector
+        // instructions, so they are issued in turn, with the LDS loads of what comes next.
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-            S[t] = gc * S[t];
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const u32x2 k0 = lds_load_tr16(K + (at_col0 ^ (4 * t << 4)) + 4096 * s);
-                const u32x2 k1 = lds_load_tr16(K + (at_col1 ^ (4 * t << 4)) + 4096 * s);
-                const u32x4 kt = {k0.x, k0.y, k1.x, k1.y};
-                S[t] = mfma_32(kt, wh[s], S[t]);
-                S[t] = mfma_32(kt, wl[s], S[t]);
+            u32x4 after[2];
+            if constexpr (OUT) {
+                o = mfma_32(sb[0], qf[t][0], o);
+                sched_fence();
+                if (t < 3) pack_rows(S[t + 1], after);
             }
+            if (t == 0) fetch_v(tile.at[1], lds.gs[gs.at[1]]);
+            if (t == 1 || t == 2) {
+                fetch_k(tile.at[0], 2 * t - 2, 1);
+                fetch_k(tile.at[0], 2 * t - 1, 1);
+            }
+            if constexpr (OUT) {
+                if (t == 3)
+#pragma unroll
+                    for (int s = 0; s < 2; ++s) ab[s] = *(const u32x4*)(lds.a[ra.at[0]] + s * 1024 + lane * 16);
+                sched_fence();
+                o = mfma_32(sb[1], qf[t][1], o);
+                sched_fence();
+                sb[0] = after[0];
+                sb[1] = after[1];
+            }
+            S[t] = gc * S[t];
+            sched_fence();
         }
+        // S += K^T (weighted V), beside the weighting for the next chunk
+        Split3 next;
+        f32x16 x;
+        unrolled<24>([&](auto m) __attribute__((always_inline)) {
+            constexpr int n = m(), s = n / 12, k = n / 4 % 3, t = n % 4;
+            S[t] = mfma_32(kt[t][s], k == 0 ? w.c[s] : k == 1 ? w.b[s] : w.a[s], S[t]);
+            if constexpr (n < 8) weigh<n>(x, vw, last, next.a);
+            if constexpr (n < 8) fetch_q(tile.at[1], n / 2, n % 2);
+            if constexpr (n >= 12 && n % 2 == 0 && n < 20) fetch_k(tile.at[1], n / 2 - 6, 0);
+            if constexpr (n == 8) x = rest_of(x, next.a, neg);
+            if constexpr (n == 13) fetch_gam(lds.gs[gs.at[1]]);
+            if constexpr (n == 14) pack_rows(x, next.b);
+            if constexpr (n == 15) x = rest_of(x, next.b, neg);
+            if constexpr (n == 21) pack_rows(x, next.c);
+            sched_fence();
+            if constexpr (OUT) {
+                if constexpr (n > 8 && n <= 12) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[4 * (n - 9) + e] *= gm;
+                }
+                if constexpr (n == 12 || n == 13) o = mfma_32(n == 12 ? v0 : v1, ab[n == 13], o);
+                if constexpr (n == 19 || n == 20) {
+                    // token l & 31, element 4a + b being value column 16h + 4a + b
+                    constexpr int j = n - 19;
+                    const auto rsrc =
+                        chunk_rsrc(ob + (size_t)i * TILE_ROWS * st_v, (uint32_t)rows_of_chunk(n_tok, i) * st_v);
+                    const int at = (int)((lane & 31) * st_v) + (col0 + 16 * h) * 2;
+                    const u32x2 p = pack4(quarter(o, 2 * j)), q = pack4(quarter(o, 2 * j + 1));
+                    __builtin_amdgcn_raw_buffer_store_b128(u32x4{p.x, p.y, q.x, q.y}, rsrc, at + 16 * j, 0, 0);
+                }
+                sched_fence();
+            }
+        });
         if constexpr (!OUT) all *= gc;
-        lds_barrier();
+        w = next;
+        counted_wait();
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        sched_fence();
         tile.next();
         ra.next();
         gs.next();
