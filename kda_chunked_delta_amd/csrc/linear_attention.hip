@@ -125,9 +125,11 @@ __device__ __forceinline__ void unrolled(F f) {
 //     i + AHEAD (8 rows each), which stay in flight for AHEAD - 2 intervals;
 //     0, 1 and 2 form a tile of A of chunk i + 1 each, 3 the row values of chunk
 //     i + 2, and loads the log-decays of chunk i + AHEAD + 1.
-// Ring slots: the tiles AHEAD + 1 chunks, A 2, the row values 3.
-constexpr int AHEAD = 5;
-constexpr int N_TILE = AHEAD + 1, N_A = 2, N_GS = 3, N_G = AHEAD + 2;
+// The output leaves through LDS: the state wavefronts put theirs of chunk i into
+// a tile, and wavefronts 0 .. 3 store whole rows of it in interval i + 1.
+// Ring slots: the tiles AHEAD + 1 chunks, A and the output 2, the row values 3.
+constexpr int AHEAD = 4;
+constexpr int N_TILE = AHEAD + 1, N_A = 2, N_O = 2, N_GS = 3, N_G = AHEAD + 2;
 constexpr int LEAD = AHEAD + 1;  // intervals before chunk 0
 template <bool OUT>
 struct Lds {
@@ -135,6 +137,7 @@ struct Lds {
     alignas(16) uint8_t v[N_TILE][TILE_BYTES];
     alignas(16) uint8_t q[OUT ? N_TILE : 1][OUT ? TILE_BYTES : 16];
     alignas(16) uint8_t a[OUT ? N_A : 1][OUT ? A_BYTES : 16];
+    alignas(16) uint8_t o[OUT ? N_O : 1][OUT ? TILE_BYTES : 16];
     alignas(16) float gs[N_GS][LS_FLOATS];
     alignas(16) float g[N_G][64];  // the loads write 64 lanes; rows past the chunk hold zeros
 };
@@ -143,6 +146,7 @@ struct Lds {
 struct Work {
     const uint8_t *q, *k, *v;  // the unit's first rows of its head
     const float* g;
+    uint8_t* out;                // as v
     uint32_t st_qk, st_v, st_g;  // bytes from row to row
     int n_tok, n_chunks;
     float scale;
@@ -159,12 +163,24 @@ __device__ __forceinline__ void produce(const Work& w, Lds<OUT>& lds, int lane) 
         load_rows(rsrc, stride, 2 * ROLE, lane, to);
         load_rows(rsrc, stride, 2 * ROLE + 1, lane, to);
     };
+    // rows 8 ROLE .. of the output of chunk c (none before the first), 2 stores
+    auto store = [&](int c) __attribute__((always_inline)) {
+        const auto rsrc = chunk_rsrc(w.out + (size_t)(c < 0 ? 0 : c) * TILE_ROWS * w.st_v,
+                                     (uint32_t)rows_of_chunk(w.n_tok, c) * w.st_v);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int row = 8 * ROLE + 4 * j + (lane >> 4);
+            const u32x4 x = *(const u32x4*)(lds.o[c & 1] + tile_off(row, lane & 15));
+            __builtin_amdgcn_raw_buffer_store_b128(x, rsrc, (int)(row * w.st_v + (lane & 15) * 16), 0, 0);
+        }
+    };
     // ring position j is chunk i + j
     for (int i = -LEAD; i < w.n_chunks; ++i) {
         const int c = i + AHEAD, rows = rows_of_chunk(w.n_tok, c);
         load(w.k, w.st_qk, c, rows, lds.k[tile.at[AHEAD]]);
         load(w.v, w.st_v, c, rows, lds.v[tile.at[AHEAD]]);
         if constexpr (OUT) load(w.q, w.st_qk, c, rows, lds.q[tile.at[AHEAD]]);
+        if constexpr (OUT) store(i - 1);
         if constexpr (ROLE == 3) {  // a fixed decay has st_g = 0
             const int left = rows_of_chunk(w.n_tok, c + 1);
             const uint32_t range = __builtin_amdgcn_readfirstlane(left ? (uint32_t)(left - 1) * w.st_g + 4 : 0u);
@@ -178,8 +194,8 @@ __device__ __forceinline__ void produce(const Work& w, Lds<OUT>& lds, int lane) 
             if (i + 1 >= 0 && i + 1 < w.n_chunks)
                 form_a<(ROLE > 0), (ROLE > 1)>(lds.q[tile.at[1]], lds.k[tile.at[1]], lds.gs[gs.at[1]], w.scale,
                                                lds.a[ra.at[1]], lane);
-        // the loads of the last AHEAD - 2 intervals are still on their way; those before have landed
-        constexpr int ISSUED = (OUT ? 6 : 4) + (ROLE == 3 ? 1 : 0);
+        // what the last AHEAD - 2 intervals issued may be on its way; the loads before have landed
+        constexpr int ISSUED = (OUT ? 8 : 4) + (ROLE == 3 ? 1 : 0);
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"(ISSUED * (AHEAD - 2)) : "memory");
         lds_barrier();
         tile.next();
@@ -187,6 +203,8 @@ __device__ __forceinline__ void produce(const Work& w, Lds<OUT>& lds, int lane) 
         gs.next();
         rg.next();
     }
+    if constexpr (OUT)
+        if (w.n_chunks > 0) store(w.n_chunks - 1);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS outlives the workgroup
 }
 
@@ -213,6 +231,7 @@ __global__ __launch_bounds__(kLaThreads) void la_prefill(LaArgs a) {
         w.k = (const uint8_t*)a.k + row_qk;
         w.v = (const uint8_t*)a.v + row * (D * 2);
         w.g = a.g + (a.g_fixed ? hd : row);
+        w.out = (uint8_t*)a.out + row * (D * 2);
         w.st_qk = (uint32_t)a.Hk * (D * 2);
         w.st_v = st_v;
         w.st_g = a.g_fixed ? 0u : (uint32_t)a.H * 4;
@@ -259,7 +278,6 @@ __global__ __launch_bounds__(kLaThreads) void la_prefill(LaArgs a) {
     if constexpr (OUT)
         if (wave < 4 + N_A) *(u32x2*)a_tile(lds.a[wave - 4], 0, 1, lane) = u32x2{0, 0};
     for (int i = -LEAD; i < 0; ++i) lds_barrier();
-    uint8_t* ob = (uint8_t*)a.out + (beg * a.H + hd) * (D * 2);
     Ring<N_TILE> tile;
     Ring<N_A> ra;
     Ring<N_GS> gs;
@@ -274,6 +292,7 @@ __global__ __launch_bounds__(kLaThreads) void la_prefill(LaArgs a) {
     // K^T: lane row l & 31 of tile t is channel 32t + 16 odd + 8 (i >> 2 & 1) + 4 (i >> 3) + (i & 3), i = l & 15
     const int at_col0 = opaque(tile_off(4 * h + r, 2 * odd + (c & 1)) + 8 * (c >> 1));
     const int at_col1 = opaque(tile_off(8 + 4 * h + r, 2 * odd + (c & 1)) + 8 * (c >> 1));
+    const int at_o = opaque(tile_off(lane & 31, (col0 >> 3) + 2 * h));
     const int at_v0 = opaque(tile_off(4 * h + r, (col0 >> 3) + 2 * (c & 1) + odd) + 8 * (c >> 1));
     const int at_v1 = opaque(tile_off(8 + 4 * h + r, (col0 >> 3) + 2 * (c & 1) + odd) + 8 * (c >> 1));
     auto columns = [&](const uint8_t* tile, int at0, int at1) __attribute__((always_inline)) {
@@ -377,14 +396,10 @@ __global__ __launch_bounds__(kLaThreads) void la_prefill(LaArgs a) {
                     for (int e = 0; e < 4; ++e) o[4 * (n - 9) + e] *= gm;
                 }
                 if constexpr (n == 12 || n == 13) o = mfma_32(n == 12 ? v0 : v1, ab[n == 13], o);
-                if constexpr (n == 19 || n == 20) {
-                    // token l & 31, element 4a + b being value column 16h + 4a + b
+                if constexpr (n == 19 || n == 20) {  // token l & 31, element 4a + b being value column 16h + 4a + b
                     constexpr int j = n - 19;
-                    const auto rsrc =
-                        chunk_rsrc(ob + (size_t)i * TILE_ROWS * st_v, (uint32_t)rows_of_chunk(n_tok, i) * st_v);
-                    const int at = (int)((lane & 31) * st_v) + (col0 + 16 * h) * 2;
                     const u32x2 p = pack4(quarter(o, 2 * j)), q = pack4(quarter(o, 2 * j + 1));
-                    __builtin_amdgcn_raw_buffer_store_b128(u32x4{p.x, p.y, q.x, q.y}, rsrc, at + 16 * j, 0, 0);
+                    *(u32x4*)(lds.o[i & 1] + (at_o ^ (j << 4))) = u32x4{p.x, p.y, q.x, q.y};
                 }
                 sched_fence();
             }
