@@ -17,13 +17,14 @@ __device__ __forceinline__ int tile_swz(int row) { return ((row & 3) << 2) | ((r
 __device__ __forceinline__ int tile_off(int row, int gi) { return row * 256 + ((gi ^ tile_swz(row)) << 4); }
 
 // Rows 4i .. 4i + 3 of a tile by one direct-to-LDS load. Rows past the
-// descriptor's range become zeros.
+// descriptor's range become zeros. NT: with the nontemporal hint.
+template <bool NT = false>
 __device__ __forceinline__ void load_rows(__amdgpu_buffer_rsrc_t rsrc, uint32_t stride, int i, int lane,
                                           uint8_t* tile) {
     const int row = 4 * i + (lane >> 4);
     const uint32_t off = (uint32_t)row * stride + (((lane & 15) ^ tile_swz(row)) << 4);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (__attribute__((address_space(3))) void*)(tile + 1024 * i), 16,
-                                             (int)off, 0, 0, 0);
+                                             (int)off, 0, 0, NT ? 2 : 0);
 }
 
 // Below this log2-decay a token's decay is zero in fp32 and stands for any

@@ -15,18 +15,18 @@ namespace {
 
 constexpr int32_t kMaxHeads = 1 << 17;  // 32 token rows of one tensor stay below 2^31 bytes
 
-// Cost model of a plan, microseconds on MI355X: what a chunk of a unit takes at
-// least, with output and without, and at what rate the whole chip moves the
-// bytes of a chunk (32 KiB with output, 16 without); a launch beside its
-// chunks; a segment's step of the merge.
-constexpr double kFullUs = 0.75, kPreUs = 0.5, kBytesPerUs = 4.8e6, kLaunchUs = 8.0, kMergeUs = 0.1;
+// Cost model of a plan, microseconds on MI355X, fitted to launches of 8 to 1024
+// units: what a chunk of a unit takes at least, with output and without, and at
+// what rate the whole chip moves the bytes of a chunk (32 KiB with output, 16
+// without); a launch beside its chunks; a segment's step of the merge.
+constexpr double kFullUs = 1.08, kPreUs = 0.82, kBytesPerUs = 5.0e6, kLaunchUs = 6.0, kMergeUs = 0.1;
 
 // A launch of units, H heads each: bound by the chain of the longest one, by
 // the workgroups that share a compute unit, or by memory.
 double launch_us(int64_t units, int64_t chunks, int longest, int H, int n_cus, double per_chunk, double bytes) {
     if (units == 0) return 0;
     const double n = (double)units * H, total = (double)chunks * H;
-    const double chain = n <= n_cus ? longest : std::max((double)longest, total / n_cus + 0.5 * longest);
+    const double chain = n <= n_cus ? longest : std::max((double)longest, total / n_cus + 0.9 * longest);
     return kLaunchUs + std::max(chain * per_chunk, total * bytes / kBytesPerUs);
 }
 
@@ -80,7 +80,8 @@ kda_status build(int32_t n_cus, const int32_t* cu, int32_t n_seqs, int32_t H, in
         total += nch[i];
         longest = std::max(longest, nch[i]);
     }
-    // segment length: given, or the cheapest of a geometric range
+    // segment length: given, or the cheapest that cuts the longest sequence into
+    // 2, 3, .. 64, 66, .. parts of at least four chunks
     const double t_serial = plan_us(nch, H, n_cus, 0);
     double t_cp = -1;
     int seg = 0;
@@ -89,7 +90,8 @@ kda_status build(int32_t n_cus, const int32_t* cu, int32_t n_seqs, int32_t H, in
             seg = seg_chunks;
             t_cp = plan_us(nch, H, n_cus, seg);
         } else {
-            for (int c = 4; c < longest; c += std::max(1, c / 4)) {
+            for (int n = 2; n <= longest / 4; n += std::max(1, n / 32)) {
+                const int c = (longest + n - 1) / n;
                 const double t = plan_us(nch, H, n_cus, c);
                 if (t_cp < 0 || t < t_cp) {
                     t_cp = t;
