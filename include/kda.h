@@ -695,7 +695,7 @@ typedef struct {
     const int32_t *bias_tokens;    /* [rows, n_bias] */
     const float *bias;             /* [rows, n_bias], bias_stride apart as the tokens */
     int64_t bias_stride;
-    int32_t n_bias;
+    int32_t n_bias;                /* up to 8192 */
     const uint32_t *allowed;       /* [rows, ceil(vocab / 32)]: bit t & 31 of word t >> 5 set for an allowed token */
     int64_t allowed_stride;
 } kda_logits;

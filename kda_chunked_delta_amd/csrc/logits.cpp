@@ -1,5 +1,7 @@
 // Host side of the processing of logits: argument checks and dispatch of
 // logits.hip behind the C ABI of include/kda.h.
+#include <algorithm>
+
 #include "kda_internal.h"
 #include "logits_launch.h"
 
@@ -19,10 +21,20 @@ size_t extent(int64_t rows, int64_t stride, int64_t n, size_t size) {
     return rows > 0 && n > 0 ? (size_t)((rows - 1) * stride + n) * size : 0;
 }
 
-// Logits per workgroup.
-constexpr int32_t kChunk = 8192, kSmallChunk = 2048;
-int32_t chunk_of(int64_t rows, int64_t vocab) {
-    return rows * ((vocab + kChunk - 1) / kChunk) >= 512 ? kChunk : kSmallChunk;
+// What a workgroup takes of a row: 8192 logits, or 2048 where that leaves the
+// chip with fewer than two workgroups per compute unit; with lists, whose words
+// have to fit LDS and which every workgroup of a row goes through, 16384 (8192
+// with words of 32 bits) or 4096.
+constexpr int32_t kSmallest = 2048;
+void split(LogitsArgs* a) {
+    const kda_logits& x = a->x;
+    a->lists = !x.tokens && !x.n_bias ? 0 : x.max_tokens < kLogitsShort ? 1 : 2;
+    a->threads = a->lists ? kLogitsListThreads : kLogitsThreads;
+    const int32_t large = a->lists == 1 ? 16384 : 8192, small = a->lists ? 2 * kSmallest : kSmallest;
+    a->chunk = (int64_t)x.rows * ((x.vocab + large - 1) / large) >= 512 ? large : small;
+    a->splits = (x.vocab + a->chunk - 1) / a->chunk;
+    const int32_t listed = x.tokens ? std::min(a->chunk, x.max_tokens) : 0;
+    a->lds = a->chunk * (a->lists == 1 ? 2 : 4) + (listed * 2 + 15) / 16 * 16;
 }
 
 }  // namespace
@@ -38,7 +50,8 @@ kda_status kda_logits_process_validate(const kda_logits* x) {
         return fail(KDA_ERR_INVALID, "%s: unknown dtype %d", who, (int)x->dtype);
     if (x->max_tokens < 0 || x->max_tokens >= 1 << 30)
         return fail(KDA_ERR_INVALID, "%s: max_tokens must be in [0, 2^30) (got %d)", who, x->max_tokens);
-    if (x->n_bias < 0) return fail(KDA_ERR_INVALID, "%s: n_bias must be >= 0 (got %d)", who, x->n_bias);
+    if (x->n_bias < 0 || x->n_bias > kLogitsBiasMax)
+        return fail(KDA_ERR_INVALID, "%s: n_bias must be in [0, %d] (got %d)", who, kLogitsBiasMax, x->n_bias);
     if (x->row_stride < x->vocab || x->out_stride < x->vocab)
         return fail(KDA_ERR_INVALID, "%s: row_stride and out_stride must be at least vocab (got %lld, %lld)", who,
                     (long long)x->row_stride, (long long)x->out_stride);
@@ -56,7 +69,7 @@ kda_status kda_logits_process_validate(const kda_logits* x) {
         x->allowed_stride > most)
         return fail(KDA_ERR_INVALID, "%s: strides must be at most 2^40", who);
     if (!x->tokens && x->max_tokens > 0) return fail(KDA_ERR_INVALID, "%s: tokens is NULL", who);
-    const int64_t splits = ((int64_t)x->vocab + kSmallChunk - 1) / kSmallChunk;  // at most so many
+    const int64_t splits = ((int64_t)x->vocab + kSmallest - 1) / kSmallest;  // at most so many
     if (!launchable(x->rows * splits, kLogitsThreads)) return fail(KDA_ERR_INVALID, "%s: rows * vocab too large", who);
     if (x->rows == 0) return KDA_OK;
     const size_t size = x->dtype == KDA_FP32 ? 4 : 2, R = (size_t)x->rows;
@@ -91,11 +104,11 @@ kda_status kda_logits_process(kda_ctx* ctx, const kda_logits* x, hipStream_t str
     if (!ctx) return fail(KDA_ERR_INVALID, "kda_logits_process: ctx is NULL");
     const kda_status st = kda_logits_process_validate(x);
     if (st != KDA_OK || x->rows == 0) return st;
-    LogitsArgs a{*x, 0, 0};
+    LogitsArgs a{};
+    a.x = *x;
     if (a.x.max_tokens == 0) a.x.tokens = nullptr;
     if (a.x.logits == a.x.out && !a.x.tokens && !a.x.n_bias && !a.x.allowed) return KDA_OK;  // nothing changes
-    a.chunk = chunk_of(a.x.rows, a.x.vocab);
-    a.splits = (a.x.vocab + a.chunk - 1) / a.chunk;
+    split(&a);
     std::lock_guard<std::mutex> lk(ctx->mu);
     DeviceScope scope;
     hipError_t e = scope.enter(ctx->device);
