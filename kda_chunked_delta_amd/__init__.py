@@ -1059,10 +1059,14 @@ def beam_select(logits, scores, n=None, finished=None, eos=None):
 
 def _rows(name, t, dtype, lead, device):
     """(address, entries of a row, row stride) of a list per row: [*lead, n], rows at one even distance."""
-    if t.dtype != dtype or t.shape[:-1] != lead or t.get_device() != device:
+    shape = t.shape
+    if t.dtype != dtype or shape[:-1] != lead or t.get_device() != device:
         raise ValueError("%s must be a %s tensor [%s, n] on cuda:%d (got %s %s on %s)"
                          % (name, dtype, ", ".join(map(str, lead)), device, t.dtype, tuple(t.shape), t.device))
-    stride, n = t.stride(), t.shape[-1]
+    n = shape[-1]
+    if t.is_contiguous():
+        return t.data_ptr(), n, n
+    stride = t.stride()
     if lead.numel() <= 1:
         row = n
     else:
@@ -1091,7 +1095,7 @@ def logits_process(logits, tokens=None, lengths=None, prompt_lengths=None, repet
     prompt; entries outside the vocabulary (-1) are skipped. With [B, W, V]
     logits, [R] stands for [B, W]. Lists and masks may be expanded over all rows.
     out: a tensor like logits, or logits itself (in place: only what changes is
-    touched); by default a new one, whose rows are padded to 16 bytes. Returns out.
+    touched); by default a new one, whose rows are padded to 128 bytes. Returns out.
     """
     import torch
     dev = logits.get_device()
@@ -1104,16 +1108,20 @@ def logits_process(logits, tokens=None, lengths=None, prompt_lengths=None, repet
         raise ValueError("logits have an empty vocabulary")
     a = Logits()
     a.rows, a.vocab, a.dtype = lead.numel(), V, dtype
+    a.logits, _, a.row_stride = _rows("logits", logits, logits.dtype, lead, dev)
     if out is None:
-        step = 4 if dtype == 0 else 8
-        if V % step:
-            out = torch.empty(*lead, -(-V // step) * step, dtype=logits.dtype, device=logits.device)[..., :V]
-        else:
-            out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        step = 32 if dtype == 0 else 64  # rows of whole 128-byte lines
+        a.out_stride = -(-V // step) * step
+        out = torch.empty(*lead, a.out_stride, dtype=logits.dtype, device=logits.device)
+        a.out = out.data_ptr()
+        if a.out_stride != V:
+            out = out[..., :V]
+    elif out is logits:
+        a.out, a.out_stride = a.logits, a.row_stride
     elif out.shape != logits.shape:
         raise ValueError("out must be like logits, %s (got %s)" % (tuple(logits.shape), tuple(out.shape)))
-    a.logits, _, a.row_stride = _rows("logits", logits, logits.dtype, lead, dev)
-    a.out, _, a.out_stride = _rows("out", out, logits.dtype, lead, dev)
+    else:
+        a.out, _, a.out_stride = _rows("out", out, logits.dtype, lead, dev)
     if tokens is not None:
         a.tokens, a.max_tokens, a.token_stride = _rows("tokens", tokens, torch.int32, lead, dev)
         for name, t, dt in (("lengths", lengths, torch.int32), ("prompt_lengths", prompt_lengths, torch.int32),

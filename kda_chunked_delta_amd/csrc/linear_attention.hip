@@ -31,8 +31,10 @@ static_assert(kLaChunk == TILE_ROWS);
 // exp(G) and exp(G_31 - G).
 constexpr int LS_H = 0, LS_L = 32, LS_GAM = 64, LS_LAST = 96, LS_FLOATS = 128;
 
-// One wavefront: x = the log-decay of row lane & 31.
-__device__ __forceinline__ void row_scan(float x, int lane, float* gs) {
+// One wavefront: x = the log-decay of row lane & 31, after the log2-decay of the
+// tokens behind the chunk, which the last values get in addition. Returns the
+// chunk's log2-decay.
+__device__ __forceinline__ double row_scan(float x, double after, int lane, float* gs) {
     const int r = lane & 31;
     x *= LOG2E;
     double G = x < LOG2_FLOOR ? LOG2_FLOOR : x;
@@ -47,8 +49,9 @@ __device__ __forceinline__ void row_scan(float x, int lane, float* gs) {
         gs[LS_H + r] = hi;
         gs[LS_L + r] = (float)(G - (double)hi);
         gs[LS_GAM + r] = exp2_hw(hi);
-        gs[LS_LAST + r] = exp2_hw((float)(all - G));
+        gs[LS_LAST + r] = exp2_hw((float)(all - G + after));
     }
+    return all;
 }
 
 // Rows lane & 31 of a tile, the granule of step s of channel tile t: 4t + 2s + h.
@@ -127,6 +130,10 @@ __device__ __forceinline__ void unrolled(F f) {
 //     i + 2, and loads the log-decays of chunk i + AHEAD + 1.
 // The output leaves through LDS: the state wavefronts put theirs of chunk i into
 // a tile, and wavefronts 0 .. 3 store whole rows of it in interval i + 1.
+// Without OUT (a segment's end state from zero) the chunks are taken from the
+// last to the first, V weighted by the decay up to the segment's end: the state
+// is never scaled, and the workgroup stops where that decay is zero in fp32
+// (below 2^-160), after a few chunks of a head that forgets fast.
 // Ring slots: the tiles AHEAD + 1 chunks, A and the output 2, the row values 3.
 constexpr int AHEAD = 4;
 constexpr int N_TILE = AHEAD + 1, N_A = 2, N_O = 2, N_GS = 3, N_G = AHEAD + 2;
@@ -140,6 +147,7 @@ struct Lds {
     alignas(16) uint8_t o[OUT ? N_O : 1][OUT ? TILE_BYTES : 16];
     alignas(16) float gs[N_GS][LS_FLOATS];
     alignas(16) float g[N_G][64];  // the loads write 64 lanes; rows past the chunk hold zeros
+    int stop;                      // without OUT: the step from which on no token counts
 };
 
 // What a workgroup works on (uniform).
@@ -150,6 +158,7 @@ struct Work {
     uint32_t st_qk, st_v, st_g;  // bytes from row to row
     int n_tok, n_chunks;
     float scale;
+    float* decay;  // without OUT: gets the decay over the unit's tokens
 };
 
 template <int ROLE, bool OUT, bool NT>
@@ -158,8 +167,11 @@ __device__ __forceinline__ void produce(const Work& w, Lds<OUT>& lds, int lane) 
     Ring<N_A> ra;
     Ring<N_GS> gs;
     Ring<N_G> rg;
-    auto load = [&](const uint8_t* base, uint32_t stride, int c, int rows, uint8_t* to) __attribute__((always_inline)) {
-        const auto rsrc = chunk_rsrc(base + (size_t)(c < 0 ? 0 : c) * TILE_ROWS * stride, (uint32_t)rows * stride);
+    // the chunk of step c
+    auto place = [&](int c) { return OUT ? c : w.n_chunks - 1 - c; };
+    auto load = [&](const uint8_t* base, uint32_t stride, int at, int rows, uint8_t* to)
+                    __attribute__((always_inline)) {
+        const auto rsrc = chunk_rsrc(base + (size_t)(at < 0 ? 0 : at) * TILE_ROWS * stride, (uint32_t)rows * stride);
         load_rows<NT>(rsrc, stride, 2 * ROLE, lane, to);
         load_rows<NT>(rsrc, stride, 2 * ROLE + 1, lane, to);
     };
@@ -175,21 +187,33 @@ __device__ __forceinline__ void produce(const Work& w, Lds<OUT>& lds, int lane) 
                                                    NT ? 2 : 0);
         }
     };
-    // ring position j is chunk i + j
-    for (int i = -LEAD; i < w.n_chunks; ++i) {
-        const int c = i + AHEAD, rows = rows_of_chunk(w.n_tok, c);
-        load(w.k, w.st_qk, c, rows, lds.k[tile.at[AHEAD]]);
-        load(w.v, w.st_v, c, rows, lds.v[tile.at[AHEAD]]);
-        if constexpr (OUT) load(w.q, w.st_qk, c, rows, lds.q[tile.at[AHEAD]]);
+    double after = 0.0;  // ROLE 3 without OUT: the log2-decay of the chunks scanned
+    int end = w.n_chunks;
+    if constexpr (ROLE == 3 && !OUT) lds.stop = end;
+    // ring position j is step i + j
+    for (int i = -LEAD; i < end; ++i) {
+        const int c = i + AHEAD, at = place(c), rows = rows_of_chunk(w.n_tok, at);
+        load(w.k, w.st_qk, at, rows, lds.k[tile.at[AHEAD]]);
+        load(w.v, w.st_v, at, rows, lds.v[tile.at[AHEAD]]);
+        if constexpr (OUT) load(w.q, w.st_qk, at, rows, lds.q[tile.at[AHEAD]]);
         if constexpr (OUT) store(i - 1);
         if constexpr (ROLE == 3) {  // a fixed decay has st_g = 0
-            const int left = rows_of_chunk(w.n_tok, c + 1);
+            const int at_g = place(c + 1), left = rows_of_chunk(w.n_tok, at_g);
             const uint32_t range = __builtin_amdgcn_readfirstlane(left ? (uint32_t)(left - 1) * w.st_g + 4 : 0u);
-            const auto rsrc = chunk_rsrc((const uint8_t*)w.g + (size_t)(c + 1) * TILE_ROWS * w.st_g, range);
+            const auto rsrc =
+                chunk_rsrc((const uint8_t*)w.g + (size_t)(at_g < 0 ? 0 : at_g) * TILE_ROWS * w.st_g, range);
             const uint32_t off = lane < left ? (uint32_t)lane * w.st_g : 0x7ffffffcu;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
                 rsrc, (__attribute__((address_space(3))) void*)lds.g[rg.at[AHEAD + 1]], 4, (int)off, 0, 0, 0);
-            if (i + 2 >= 0 && i + 2 < w.n_chunks) row_scan(lds.g[rg.at[2]][lane & 31], lane, lds.gs[gs.at[2]]);
+            if (i + 2 >= 0 && i + 2 < end) {
+                if (!OUT && after <= LOG2_FLOOR) {
+                    end = i + 2;
+                    lds.stop = end;
+                } else {
+                    const double all = row_scan(lds.g[rg.at[2]][lane & 31], after, lane, lds.gs[gs.at[2]]);
+                    if constexpr (!OUT) after += all;
+                }
+            }
         }
         if constexpr (ROLE < 3 && OUT)  // tiles (0, 0), (1, 0) and (1, 1)
             if (i + 1 >= 0 && i + 1 < w.n_chunks)
@@ -199,13 +223,17 @@ __device__ __forceinline__ void produce(const Work& w, Lds<OUT>& lds, int lane) 
         constexpr int ISSUED = (OUT ? 8 : 4) + (ROLE == 3 ? 1 : 0);
         asm volatile("s_waitcnt vmcnt(%0)" ::"n"(ISSUED * (AHEAD - 2)) : "memory");
         lds_barrier();
+        if constexpr (ROLE != 3 && !OUT) end = __builtin_amdgcn_readfirstlane(lds.stop);
         tile.next();
         ra.next();
         gs.next();
         rg.next();
     }
-    if constexpr (OUT)
+    if constexpr (OUT) {
         if (w.n_chunks > 0) store(w.n_chunks - 1);
+    } else if constexpr (ROLE == 3) {
+        if (lane == 0) *w.decay = exp2_hw((float)after);
+    }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS outlives the workgroup
 }
 
@@ -239,6 +267,7 @@ __global__ __launch_bounds__(kLaThreads) void la_prefill(LaArgs a) {
         w.n_tok = n_tok;
         w.n_chunks = n_chunks;
         w.scale = a.scale;
+        w.decay = OUT ? nullptr : a.decays + (int64_t)un.out * a.H + hd;
         if (wave == 0) produce<0, OUT, NT>(w, lds, lane);
         else if (wave == 1) produce<1, OUT, NT>(w, lds, lane);
         else if (wave == 2) produce<2, OUT, NT>(w, lds, lane);
@@ -288,7 +317,6 @@ __global__ __launch_bounds__(kLaThreads) void la_prefill(LaArgs a) {
         ra.next();
         gs.next();
     }
-    float all = 1.f;  // the decay over the unit's tokens
     const int at_row = opaque(tile_off(lane & 31, h));
     // K^T: lane row l & 31 of tile t is channel 32t + 16 odd + 8 (i >> 2 & 1) + 4 (i >> 3) + (i & 3), i = l & 15
     const int at_col0 = opaque(tile_off(4 * h + r, 2 * odd + (c & 1)) + 8 * (c >> 1));
@@ -313,9 +341,14 @@ __global__ __launch_bounds__(kLaThreads) void la_prefill(LaArgs a) {
         for (int a = 0; a < 4; ++a) last[a] = *(const f32x4*)(row + LS_LAST + 8 * a + 4 * h);
     };
     float gam_all, gam_row = 0.f;
+    int n_steps = n_chunks;
     auto fetch_gam = [&](const float* row) __attribute__((always_inline)) {
-        gam_all = row[LS_GAM + 31];
-        if constexpr (OUT) gam_row = a.scale * row[LS_GAM + (lane & 31)];
+        if constexpr (OUT) {
+            gam_all = row[LS_GAM + 31];
+            gam_row = a.scale * row[LS_GAM + (lane & 31)];
+        } else {
+            n_steps = lds.stop;
+        }
     };
     auto fetch_q = [&](int slot, int t, int s) __attribute__((always_inline)) {
         if constexpr (OUT) qf[t][s] = row32(lds.q[slot], at_row, t, s);
@@ -341,8 +374,8 @@ __global__ __launch_bounds__(kLaThreads) void la_prefill(LaArgs a) {
         pack_rows(x, w.c);
     }
     counted_wait();
-    for (int i = 0; i < n_chunks; ++i) {
-        const float gc = gam_all, gm = gam_row;
+    for (int i = 0; i < (OUT ? n_chunks : __builtin_amdgcn_readfirstlane(n_steps)); ++i) {
+        const float gc = OUT ? gam_all : 1.f, gm = gam_row;
         const u32x4 v0 = vw[0], v1 = vw[1];
         u32x4 ab[2], sb[2];
         f32x16 o = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -373,7 +406,7 @@ __global__ __launch_bounds__(kLaThreads) void la_prefill(LaArgs a) {
                 sb[0] = after[0];
                 sb[1] = after[1];
             }
-            S[t] = gc * S[t];
+            if constexpr (OUT) S[t] = gc * S[t];
             sched_fence();
         }
         // S += K^T (weighted V), beside the weighting for the next chunk
@@ -405,7 +438,6 @@ __global__ __launch_bounds__(kLaThreads) void la_prefill(LaArgs a) {
                 sched_fence();
             }
         });
-        if constexpr (!OUT) all *= gc;
         w = next;
         counted_wait();
         __builtin_amdgcn_s_barrier();
@@ -418,7 +450,6 @@ __global__ __launch_bounds__(kLaThreads) void la_prefill(LaArgs a) {
     if (un.out >= 0) {
         float* p = a.slots + ((int64_t)un.out * a.H + hd) * (D * D);
         each([&](int at, float s) { return p[at] = s; });
-        if (threadIdx.x == kLaThreads - 1) a.decays[(int64_t)un.out * a.H + hd] = all;
     } else if (un.out == LA_FINAL && a.sT) {
         if (a.state_bf16) {
             uint16_t* p = (uint16_t*)a.sT + own;
