@@ -701,8 +701,8 @@ typedef struct {
 } kda_logits;
 
 /* One launch on `stream`, no workspace, no allocation, no synchronisation;
- * results are bitwise reproducible. rows times the chunks of 2048 logits of a row
- * are fewer than 2^24. */
+ * results are bitwise reproducible. rows times the chunks of 4096 logits of a row
+ * are fewer than 2^23. */
 kda_status kda_logits_process(kda_ctx *ctx, const kda_logits *args, hipStream_t stream);
 
 /* The argument checks of kda_logits_process (addresses only; no GPU). */
