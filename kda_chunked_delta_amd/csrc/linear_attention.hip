@@ -17,6 +17,8 @@
 //   - A and the copy of S that Q S multiplies become one bf16 each (2^-9): they
 //     only reach the output, which is bf16 itself.
 // All sums are fp32, the running sum of g is fp64 (differences of it are taken).
+// An fp32 state ends within 3e-7 of the exact one (its norm); plain fp32
+// arithmetic within 2e-7.
 #include "chunk_tiles.hpp"
 #include "linear_attention_launch.h"
 
@@ -112,6 +114,7 @@ __device__ __forceinline__ void weigh(f32x16& x, const u32x4 (&v)[2], const f32x
     to[N >> 2][N & 3] = pack_bf16(x[2 * N], x[2 * N + 1]);
 }
 
+// f(0), f(1), .. f(N - 1) with the number as a constant.
 template <int N, class F>
 __device__ __forceinline__ void unrolled(F f) {
     if constexpr (N > 0) {
@@ -135,6 +138,23 @@ __device__ __forceinline__ void unrolled(F f) {
 // is never scaled, and the workgroup stops where that decay is zero in fp32
 // (below 2^-160), after a few chunks of a head that forgets fast.
 // Ring slots: the tiles AHEAD + 1 chunks, A and the output 2, the row values 3.
+//
+// Bound by memory where every compute unit is at work: 5.0 to 5.2 TB/s of q, k, v
+// and o, what a copy of 1 GiB reaches (1.65 us a chunk for 256 workgroups; 16
+// prompts of 2048 tokens and 64 heads 416 to 440 us). With fewer workgroups by the
+// chain of chunks, 1.04 us each with 8 to 32 of them, and by what one compute unit
+// has in flight, 28 GB/s, 1.14 us with 128. The chain's 2400 cycles are 38 products
+// of 32 cycles and some 200 vector instructions of 4 on each state wavefront, which
+// its SIMD issues one after the other, and those of the operand wavefront beside it.
+// Steps that were measured, us a chunk with 8 workgroups: LDS loads next to their
+// use 1.24; loads, products and vector instructions issued in turn and a phase
+// ahead, A by three wavefronts instead of one 1.17; the state's wavefronts first on
+// their SIMD 1.06. Outputs as rows through LDS instead of 32 bytes per token and
+// wavefront: 457 to 430 us for the 16 prompts. Not better: 8 state wavefronts of 16
+// columns on 16x16x32 products (1.20 a chunk; every operand is read twice as often),
+// V in two parts instead of three (0.99 with 8 workgroups, no change at full load,
+// and 2.7e-6 of the state lost), 3 to 8 chunks of loads ahead, heads in the order of
+// the XCDs.
 constexpr int AHEAD = 4;
 constexpr int N_TILE = AHEAD + 1, N_A = 2, N_O = 2, N_GS = 3, N_G = AHEAD + 2;
 constexpr int LEAD = AHEAD + 1;  // intervals before chunk 0
@@ -467,7 +487,7 @@ __global__ __launch_bounds__(kLaThreads) void la_prefill(LaArgs a) {
 // The states between segments: slot 0 gets the initial state, and slot s + 1,
 // which holds the end state of segment s from zero, is added the decayed slot s.
 // One thread per four elements of a state; the loads of DEEP segments are in
-// flight together.
+// flight together: 32 segments of 8 heads (32 MiB) take 8 us.
 constexpr int DEEP = 8;
 static_assert(kLaMergeTiles * kLaMergeThreads * 4 == D * D);
 __global__ __launch_bounds__(kLaMergeThreads) void la_merge(LaMergeArgs a) {
@@ -509,7 +529,13 @@ __global__ __launch_bounds__(kLaMergeThreads) void la_merge(LaMergeArgs a) {
 // state in registers over all T tokens: lane (rs, cg) = (lane >> 3, lane & 7)
 // owns rows 16rs .. + 15 of columns 4cg .. + 3, so a load instruction covers
 // eight whole 128-byte lines, the sums need three lane exchanges and the
-// kernel needs neither LDS nor a barrier.
+// kernel needs neither LDS nor a barrier. Bound by HBM: 256 sequences of 32 heads
+// take 192 us (5.6 TB/s); one sequence takes 4, the latency of the launch and of
+// one load after another.
+//
+// States beyond 128 MiB, half the last-level cache, are read and written with
+// the nontemporal hint, as the gated delta rule's decode does, which moves the
+// same bytes and measured both sides.
 static_assert(kLaDecodeThreads == 64 * 4);  // a wavefront per 32-column tile
 
 template <bool NT>

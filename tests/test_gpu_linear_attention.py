@@ -2,10 +2,10 @@
 with the per-token recurrence in 64 bits: chunked prefill, segmented prefill, and
 decode of one or several tokens.
 
-Tolerances. fp32 states, relative to the norm of the exact one: what a token adds
-enters as a hi + lo bf16 pair (2^-18 of its value, at most) times a weight, the
-running decay is an fp32 product over the chunks that a state remembers (2^-22 of
-a chunk each): 1e-5 bounds 2.6 * 2^-18. Decode is fp32 throughout: 128-term sums,
+Tolerances. fp32 states, relative to the norm of the exact one: a token enters
+with 24 bits, times a weight of 2^-22 (an exponential), and the running decay is an
+fp32 product over the chunks that a state remembers, 2^-22 of each: 1e-5 bounds 40 of
+them (decays that let more count are close to one, and rounded to 2^-24). Decode is fp32 throughout: 128-term sums,
 2e-6. Outputs of the prefill are rounded three times to bf16 (the copy of the
 state, the decayed q . k products, the output), each by at most HALF = 2^-8 of
 its value. So one output is off by at most HALF of itself and of what it would be
