@@ -153,7 +153,7 @@ __device__ __forceinline__ void unrolled(F f) {
 // wavefront: 457 to 430 us for the 16 prompts. Not better: 8 state wavefronts of 16
 // columns on 16x16x32 products (1.20 a chunk; every operand is read twice as often),
 // V in two parts instead of three (0.99 with 8 workgroups, no change at full load,
-// and 2.7e-6 of the state lost), 3 to 8 chunks of loads ahead, heads in the order of
+// and 3e-6 of the state lost), 3 to 8 chunks of loads ahead, heads in the order of
 // the XCDs.
 constexpr int AHEAD = 4;
 constexpr int N_TILE = AHEAD + 1, N_A = 2, N_O = 2, N_GS = 3, N_G = AHEAD + 2;

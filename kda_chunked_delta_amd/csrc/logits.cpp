@@ -24,15 +24,16 @@ size_t extent(int64_t rows, int64_t stride, int64_t n, size_t size) {
 // What a workgroup takes of a row: 8192 logits, or 2048 where that leaves the
 // chip with fewer than two workgroups per compute unit. With lists, which every
 // workgroup of a row goes through, 16384 or 4096; 8192 in place of 16384 where
-// words of 32 bits, or the room for a history of more than 8192 tokens, would
-// pass 64 KiB of LDS. Measured with lists: 256 rows of 131072, 37 us, 39 with
-// 8192; 129 rows of 100003, 12 us, 20 with 32768.
+// words of 32 bits, or the room for a history of more than 4096 tokens, would
+// leave a compute unit fewer than four workgroups (40 KiB of LDS each). Measured
+// for 256 rows of 131072, histories of 4096 tokens: 37 us, 39 with 8192; of 8192
+// tokens (fp32): 92 with 16384, 82 with 8192.
 constexpr int32_t kSmallest = 2048;
 void split(LogitsArgs* a) {
     const kda_logits& x = a->x;
     a->lists = !x.tokens && !x.n_bias ? 0 : x.max_tokens < kLogitsShort ? 1 : 2;
     a->threads = a->lists ? kLogitsListThreads : kLogitsThreads;
-    const int32_t large = a->lists == 1 && x.max_tokens <= 8192 ? 16384 : 8192, small = a->lists ? 2 * kSmallest : kSmallest;
+    const int32_t large = a->lists == 1 && x.max_tokens <= 4096 ? 16384 : 8192, small = a->lists ? 2 * kSmallest : kSmallest;
     a->chunk = (int64_t)x.rows * ((x.vocab + large - 1) / large) >= 512 ? large : small;
     a->splits = (x.vocab + a->chunk - 1) / a->chunk;
     const int32_t listed = x.tokens ? std::min(a->chunk, x.max_tokens) : 0;
@@ -109,7 +110,8 @@ kda_status kda_logits_process(kda_ctx* ctx, const kda_logits* x, hipStream_t str
     if (st != KDA_OK || x->rows == 0) return st;
     LogitsArgs a{};
     a.x = *x;
-    if (a.x.max_tokens == 0) a.x.tokens = nullptr;
+    // a history that no penalty asks for is not looked at
+    if (a.x.max_tokens == 0 || !(a.x.repetition || a.x.frequency || a.x.presence)) a.x.tokens = nullptr;
     if (a.x.logits == a.x.out && !a.x.tokens && !a.x.n_bias && !a.x.allowed) return KDA_OK;  // nothing changes
     split(&a);
     std::lock_guard<std::mutex> lk(ctx->mu);

@@ -182,7 +182,7 @@ def test_long_histories():
     check(d, run(d), "long")
 
 
-@pytest.mark.parametrize("L", [1, 8191, 8192, 8193, 16383, 16384])
+@pytest.mark.parametrize("L", [1, 4096, 4097, 8193, 16383, 16384])
 @pytest.mark.parametrize("K", [0, 70, 8192])
 def test_room_for_histories_and_biases(L, K):
     """Histories at the borders of the word sizes and of the room for them, in calls with many rows and with few:
@@ -371,3 +371,12 @@ def test_refusals():
         kda.logits_process(buf[:, :100], out=buf[:, 100:])  # between each other's rows
     with pytest.raises(kda.KDAError):
         kda.logits_process(x, allowed=x.view(torch.int32)[:, :4], out=x)
+
+
+def test_a_history_without_penalties_changes_nothing():
+    """Not even the bits of a NaN that is no quiet one."""
+    x = torch.randn(3, 500, device=DEV).bfloat16()
+    x.view(torch.int16)[:, 7] = 0x7f81
+    t = torch.full((3, 4), 7, dtype=torch.int32, device=DEV)
+    out = kda.logits_process(x, tokens=t)
+    assert torch.equal(out.contiguous().view(torch.int16), x.view(torch.int16))
