@@ -627,14 +627,15 @@ def _packed_plan(what, make, plan, cu_seqlens, cu_seqlens_host, Tt, H, dev, use_
     cu_seqlens_host = [int(x) for x in cu_seqlens_host]
     N = len(cu_seqlens_host) - 1
     # the library sizes every buffer from the plan, so the table must describe
-    # exactly the packed tokens the tensors hold
+    # exactly the packed tokens the tensors hold (one that has a plan never decreases)
+    mode = _cp_mode(use_intracard_cp) if plan is None else None
+    known = plan is not None or (dev, tuple(cu_seqlens_host), H, mode, make) in _plan_cache
     if (N < 1 or cu_seqlens_host[0] != 0 or cu_seqlens_host[-1] != Tt
-            or any(b < a for a, b in zip(cu_seqlens_host, cu_seqlens_host[1:]))):
+            or not known and any(b < a for a, b in zip(cu_seqlens_host, cu_seqlens_host[1:]))):
         raise ValueError("cu_seqlens must start at 0, never decrease and end at the %d packed tokens (got %s)"
                          % (Tt, cu_seqlens_host[:8]))
     if plan is None:
-        mode = _cp_mode(use_intracard_cp)
-        if capturing and (dev, tuple(cu_seqlens_host), H, mode, make) not in _plan_cache:
+        if capturing and not known:
             raise ValueError("a graph capture needs a plan made before it: pass plan=plan_%s(...), or call "
                              "once with these cu_seqlens" % what)
         plan = _cached_plan(cu_seqlens_host, H, mode, dev, make)

@@ -246,7 +246,8 @@ kda_status kda_linear_attention_prefill_validate(const kda_plan* p, const kda_li
     const size_t n_state = N * H * 128 * 128 * (state16 ? 2 : 4);
     const Buffer ins[] = {{q, n_qk, "q"}, {k, n_qk, "k"}, {v, n_act, "v"}, {g, (fixed ? H : Tt * H) * 4, "g"},
                           {cu_dev, (N + 1) * 4, "cu_seqlens"}, {s0, n_state, "initial_state"}};
-    const Buffer outs[] = {{out, n_act, "out"}, {sT, n_state, "final_state"}, {workspace, in.workspace_bytes, "workspace"}};
+    const Buffer outs[] = {{out, n_act, "out"}, {sT, n_state, "final_state"},
+                           {workspace, in.workspace_bytes, "workspace"}};
     if (Tt > 0) {
         const size_t align[] = {16, 16, 16, 4};
         for (int i = 0; i < 4; ++i) {

@@ -557,13 +557,26 @@ __global__ __launch_bounds__(kLaDecodeThreads) void la_decode(LaDecodeArgs a) {
         if constexpr (NT) s[i] = __builtin_nontemporal_load(st + i * (D / 4));
         else s[i] = st[i * (D / 4)];
     }
-    for (int t = 0; t < a.T; ++t) {
+    struct Token {
+        u32x4 k[2], q[2];
+        u32x2 v;
+        float g;
+    };
+    auto load = [&](int t) __attribute__((always_inline)) {
         const int64_t row = (n * a.T + t) * a.H + hd, rq = (n * a.T + t) * a.Hk + hq;
         const u32x4* kp = (const u32x4*)(a.k + rq * D + 16 * rs);
         const u32x4* qp = (const u32x4*)(a.q + rq * D + 16 * rs);
-        const u32x4 k2[2] = {kp[0], kp[1]}, q2[2] = {qp[0], qp[1]};
-        const u32x2 vb = *(const u32x2*)(a.v + row * D + col);
-        const float gam = exp2_hw(a.g[a.g_fixed ? hd : row] * LOG2E);
+        return Token{{kp[0], kp[1]}, {qp[0], qp[1]}, *(const u32x2*)(a.v + row * D + col),
+                     a.g[a.g_fixed ? hd : row]};
+    };
+    Token next = load(0);  // each a token ahead
+    for (int t = 0; t < a.T; ++t) {
+        const int64_t row = (n * a.T + t) * a.H + hd;
+        const Token now = next;
+        if (t + 1 < a.T) next = load(t + 1);
+        const u32x4 (&k2)[2] = now.k, (&q2)[2] = now.q;
+        const u32x2 vb = now.v;
+        const float gam = exp2_hw(now.g * LOG2E);
         float k[16], q[16], qk = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {

@@ -33,7 +33,8 @@ void split(LogitsArgs* a) {
     const kda_logits& x = a->x;
     a->lists = !x.tokens && !x.n_bias ? 0 : x.max_tokens < kLogitsShort ? 1 : 2;
     a->threads = a->lists ? kLogitsListThreads : kLogitsThreads;
-    const int32_t large = a->lists == 1 && x.max_tokens <= 4096 ? 16384 : 8192, small = a->lists ? 2 * kSmallest : kSmallest;
+    const int32_t large = a->lists == 1 && x.max_tokens <= 4096 ? 16384 : 8192;
+    const int32_t small = a->lists ? 2 * kSmallest : kSmallest;
     a->chunk = (int64_t)x.rows * ((x.vocab + large - 1) / large) >= 512 ? large : small;
     a->splits = (x.vocab + a->chunk - 1) / a->chunk;
     const int32_t listed = x.tokens ? std::min(a->chunk, x.max_tokens) : 0;

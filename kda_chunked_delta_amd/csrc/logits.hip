@@ -169,7 +169,8 @@ __global__ __launch_bounds__(THREADS) void process_logits(LogitsArgs a) {
             if (a.x.frequency) r.frequency = a.x.frequency[row];
             if (a.x.presence) r.presence = a.x.presence[row];
         }
-        for (int i = tid * 16; i < n * (W::BITS / 8); i += THREADS * 16) *(u32x4*)((uint8_t*)lds + i) = u32x4{0, 0, 0, 0};
+        for (int i = tid * 16; i < n * (W::BITS / 8); i += THREADS * 16)
+            *(u32x4*)((uint8_t*)lds + i) = u32x4{0, 0, 0, 0};
         if (tid == 0) n_list = 0;
         __syncthreads();
         if (bias_tokens) {
