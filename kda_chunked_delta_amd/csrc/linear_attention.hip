@@ -14,8 +14,10 @@
 //   - diag(exp(G_31 - G)) V becomes the sum of three bf16 numbers, all 24 bits of
 //     its mantissa, since the state keeps its sum: one bf16 would leave 2^-9 of
 //     each token in an fp32 state, two 2^-18;
-//   - A and the copy of S that Q S multiplies become one bf16 each (2^-9): they
-//     only reach the output, which is bf16 itself.
+//   - A becomes a pair hi + lo (2^-17): a rounding of one of its few large values
+//     would reach a whole row of an output, and not average out;
+//   - the copy of S that Q S multiplies becomes one bf16 (2^-8 at most of each
+//     value): a sum over its 128 channels reaches the output, which is bf16 itself.
 // All sums are fp32, the running sum of g is fp64 (differences of it are taken).
 // An fp32 state ends within 3e-7 of the exact one (its norm); plain fp32
 // arithmetic within 2e-7.
@@ -61,12 +63,12 @@ __device__ __forceinline__ u32x4 row32(const uint8_t* tile, int at_row, int t, i
     return *(const u32x4*)(tile + (at_row ^ ((4 * t + 2 * s) << 4)));
 }
 
-// A of a chunk as the operand of A V: [step s 2][lane 64][8 bf16], lane l
-// holding token l & 31 and the keys 16s + 8 (j >> 2) + 4 (l >> 5) + (j & 3).
+// A of a chunk as the operand of A V, hi and lo: [2][step s 2][lane 64][8 bf16], lane
+// l holding token l & 31 and the keys 16s + 8 (j >> 2) + 4 (l >> 5) + (j & 3).
 // One wavefront forms the 16 x 16 tile of tokens 16 rt .. and keys 16 ct .. :
 // lane (gg, m) has token 16 rt + m and keys 16 ct + 4 gg + b, half a lane's
 // entry. Tile (0, 1) is zero; it is cleared once and never written.
-constexpr int A_BYTES = 2048;
+constexpr int A_LO = 2048, A_BYTES = 4096;
 __device__ __forceinline__ uint8_t* a_tile(uint8_t* rec, int rt, int ct, int lane) {
     const int gg = lane >> 4, m = lane & 15;
     return rec + ct * 1024 + (32 * (gg & 1) + 16 * rt + m) * 16 + 8 * (gg >> 1);
@@ -86,7 +88,9 @@ __device__ __forceinline__ void form_a(const uint8_t* Q, const uint8_t* K, const
 #pragma unroll
     for (int b = 0; b < 4; ++b)
         x[b] = CT < RT || 4 * gg + b <= m ? scale * x[b] * pair_decay(hm, lm, hv[b], lv[b]) : 0.f;
-    *(u32x2*)a_tile(rec, RT, CT, lane) = pack4(x);
+    const HiLo y = split4(x);
+    *(u32x2*)a_tile(rec, RT, CT, lane) = y.h;
+    *(u32x2*)(a_tile(rec, RT, CT, lane) + A_LO) = y.l;
 }
 
 // A wait for the wavefront's LDS traffic that the compiler counts: it then knows
@@ -143,7 +147,7 @@ __device__ __forceinline__ void unrolled(F f) {
 // and o, what a copy of 1 GiB reaches (1.65 us a chunk for 256 workgroups; 16
 // prompts of 2048 tokens and 64 heads 416 to 440 us). With fewer workgroups by the
 // chain of chunks, 1.04 us each with 8 to 32 of them, and by what one compute unit
-// has in flight, 28 GB/s, 1.14 us with 128. The chain's 2400 cycles are 38 products
+// has in flight, 28 GB/s, 1.14 us with 128. The chain's 2400 cycles are 40 products
 // of 32 cycles and some 200 vector instructions of 4 on each state wavefront, which
 // its SIMD issues one after the other, and those of the operand wavefront beside it.
 // Steps that were measured, us a chunk with 8 workgroups: LDS loads next to their
@@ -326,7 +330,9 @@ __global__ __launch_bounds__(kLaThreads) void la_prefill(LaArgs a) {
         each([&](int, float) { return 0.f; });
     }
     if constexpr (OUT)
-        if (wave < 4 + N_A) *(u32x2*)a_tile(lds.a[wave - 4], 0, 1, lane) = u32x2{0, 0};
+        if (wave < 4 + N_A)
+            for (int part = 0; part < A_BYTES; part += A_LO)
+                *(u32x2*)(a_tile(lds.a[wave - 4], 0, 1, lane) + part) = u32x2{0, 0};
     for (int i = -LEAD; i < 0; ++i) lds_barrier();
     Ring<N_TILE> tile;
     Ring<N_A> ra;
@@ -397,7 +403,7 @@ __global__ __launch_bounds__(kLaThreads) void la_prefill(LaArgs a) {
     for (int i = 0; i < (OUT ? n_chunks : __builtin_amdgcn_readfirstlane(n_steps)); ++i) {
         const float gc = OUT ? gam_all : 1.f, gm = gam_row;
         const u32x4 v0 = vw[0], v1 = vw[1];
-        u32x4 ab[2], sb[2];
+        u32x4 ah[2], al[2], sb[2];
         f32x16 o = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if constexpr (OUT) pack_rows(S[0], sb);
         sched_fence();
@@ -417,9 +423,6 @@ __global__ __launch_bounds__(kLaThreads) void la_prefill(LaArgs a) {
                 fetch_k(tile.at[0], 2 * t - 1, 1);
             }
             if constexpr (OUT) {
-                if (t == 3)
-#pragma unroll
-                    for (int s = 0; s < 2; ++s) ab[s] = *(const u32x4*)(lds.a[ra.at[0]] + s * 1024 + lane * 16);
                 sched_fence();
                 o = mfma_32(sb[1], qf[t][1], o);
                 sched_fence();
@@ -445,11 +448,17 @@ __global__ __launch_bounds__(kLaThreads) void la_prefill(LaArgs a) {
             if constexpr (n == 21) pack_rows(x, next.c);
             sched_fence();
             if constexpr (OUT) {
+                if constexpr (n == 8 || n == 9) {
+                    constexpr int at = (n - 8) * 1024;
+                    ah[n - 8] = *(const u32x4*)(lds.a[ra.at[0]] + at + lane * 16);
+                    al[n - 8] = *(const u32x4*)(lds.a[ra.at[0]] + A_LO + at + lane * 16);
+                }
                 if constexpr (n > 8 && n <= 12) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[4 * (n - 9) + e] *= gm;
                 }
-                if constexpr (n == 12 || n == 13) o = mfma_32(n == 12 ? v0 : v1, ab[n == 13], o);
+                if constexpr (n == 12 || n == 13) o = mfma_32(n == 12 ? v0 : v1, al[n == 13], o);
+                if constexpr (n == 14 || n == 15) o = mfma_32(n == 14 ? v0 : v1, ah[n == 15], o);
                 if constexpr (n == 19 || n == 20) {  // token l & 31, element 4a + b being value column 16h + 4a + b
                     constexpr int j = n - 19;
                     const u32x2 p = pack4(quarter(o, 2 * j)), q = pack4(quarter(o, 2 * j + 1));

@@ -6,12 +6,11 @@ Tolerances. fp32 states, relative to the norm of the exact one: a token enters
 with 24 bits, times a weight of 2^-22 (an exponential), and the running decay is an
 fp32 product over the chunks that a state remembers, 2^-22 of each: 1e-5 bounds 40 of
 them (decays that let more count are close to one, and rounded to 2^-24). Decode is fp32 throughout: 128-term sums,
-2e-6. Outputs of the prefill are rounded three times to bf16 (the copy of the
-state, the decayed q . k products, the output), each by at most HALF = 2^-8 of
-its value. So one output is off by at most HALF of itself and of what it would be
-with all signs positive (which bounds both sums); and over many independent
-outputs each rounding has an rms of HALF / sqrt(3) at most, of which the first
-two share the terms of one sum: sqrt(2 / 3) HALF in the norm, held to HALF.
+2e-6. Outputs of the prefill are rounded twice to bf16 (the copy of the state,
+the output), each by at most HALF = 2^-8 of its value; the decayed q . k products
+are pairs, 2^-17. So one output is off by at most HALF of itself and of what it
+would be with all signs positive; and over many independent outputs each rounding
+has an rms of HALF / sqrt(3) at most: sqrt(2 / 3) HALF in the norm, held to HALF.
 Outputs of the decode are rounded once."""
 import math
 
