@@ -504,9 +504,9 @@ kda_status kda_gated_delta_decode_validate(int32_t n_seqs, int32_t n_tokens, int
  * state enters with all 24 bits of its mantissa: an fp32 state is within 1e-6 of
  * the exact one relative to its norm (3e-7 measured, plain fp32 arithmetic is within
  * about 2e-7). The copy of the state that an output reads is rounded to bf16 once,
- * as the output is. Decoding is fp32 throughout. All other inputs have to be finite: a value that is not reaches
- * the results of its own sequence and head from its chunk of 32 tokens on, that
- * is also of up to 31 tokens before it.
+ * as the output is. Decoding is fp32 throughout. All other inputs have to be
+ * finite: a value that is not reaches the results of its own sequence and head from
+ * its chunk of 32 tokens on, that is also of up to 31 tokens before it.
  * ------------------------------------------------------------------------- */
 
 /* Build the plan of a packed batch for kda_linear_attention_prefill: as
