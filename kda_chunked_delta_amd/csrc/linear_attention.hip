@@ -143,11 +143,11 @@ __device__ __forceinline__ void unrolled(F f) {
 // (below 2^-160), after a few chunks of a head that forgets fast.
 // Ring slots: the tiles AHEAD + 1 chunks, A and the output 2, the row values 3.
 //
-// Bound by memory where every compute unit is at work: 5.0 to 5.2 TB/s of q, k, v
-// and o, what a copy of 1 GiB reaches (1.65 us a chunk for 256 workgroups; 16
-// prompts of 2048 tokens and 64 heads 416 to 440 us). With fewer workgroups by the
-// chain of chunks, 1.04 us each with 8 to 32 of them, and by what one compute unit
-// has in flight, 28 GB/s, 1.14 us with 128. The chain's 2400 cycles are 40 products
+// Bound by memory where every compute unit is at work: 4.8 to 4.95 TB/s of q, k, v
+// and o, where a copy of 1 GiB reaches 5.15 (1.7 us a chunk for 256 workgroups; 16
+// prompts of 2048 tokens and 64 heads 435 to 447 us, 3% less without A's second part). With fewer workgroups by the
+// chain of chunks, 1.05 us each with 8 to 32 of them, and by what one compute unit
+// has in flight, 28 GB/s, 1.18 us with 128. The chain's 2400 cycles are 40 products
 // of 32 cycles and some 200 vector instructions of 4 on each state wavefront, which
 // its SIMD issues one after the other, and those of the operand wavefront beside it.
 // Steps that were measured, us a chunk with 8 workgroups: LDS loads next to their
@@ -539,7 +539,7 @@ __global__ __launch_bounds__(kLaMergeThreads) void la_merge(LaMergeArgs a) {
 // owns rows 16rs .. + 15 of columns 4cg .. + 3, so a load instruction covers
 // eight whole 128-byte lines, the sums need three lane exchanges and the
 // kernel needs neither LDS nor a barrier. Bound by HBM: 256 sequences of 32 heads
-// take 192 us (5.6 TB/s); one sequence takes 4, the latency of the launch and of
+// take 188 us (5.7 TB/s); one sequence takes 4, the latency of the launch and of
 // one load after another.
 //
 // States beyond 128 MiB, half the last-level cache, are read and written with
