@@ -143,12 +143,12 @@ __device__ __forceinline__ void unrolled(F f) {
 // (below 2^-160), after a few chunks of a head that forgets fast.
 // Ring slots: the tiles AHEAD + 1 chunks, A and the output 2, the row values 3.
 //
-// Bound by memory where every compute unit is at work: 4.8 to 4.95 TB/s of q, k, v
+// Bound by memory where every compute unit is at work: 4.65 to 4.95 TB/s of q, k, v
 // and o, where a copy of 1 GiB reaches 5.15 (1.7 us a chunk for 256 workgroups; 16
-// prompts of 2048 tokens and 64 heads 435 to 447 us, 3% less without A's second part). With fewer workgroups by the
-// chain of chunks, 1.05 us each with 8 to 32 of them, and by what one compute unit
-// has in flight, 28 GB/s, 1.18 us with 128. The chain's 2400 cycles are 40 products
-// of 32 cycles and some 200 vector instructions of 4 on each state wavefront, which
+// prompts of 2048 tokens and 64 heads 435 to 461 us, 3 to 4% less without A's
+// second part). With fewer workgroups by the chain of chunks, 1.05 us each with 8
+// to 32 of them, and by what one compute unit has in flight, 28 GB/s, 1.18 us with
+// 128. The chain's 2400 cycles are 36 products of 32 cycles and some 200 vector instructions of 4 on each state wavefront, which
 // its SIMD issues one after the other, and those of the operand wavefront beside it.
 // Steps that were measured, us a chunk with 8 workgroups: LDS loads next to their
 // use 1.24; loads, products and vector instructions issued in turn and a phase
