@@ -1087,8 +1087,8 @@ def logits_process(logits, tokens=None, lengths=None, prompt_lengths=None, repet
         tokens of the history;
       frequency, presence, fp32 [R]: x - (frequency m + presence) for the tokens
         that stand m > 0 times in the history past its prompt;
-      bias, fp32 [R, K], of the tokens bias_tokens, int32 [R, K]: x + bias (of
-        several for one token the last);
+      bias, fp32 [R, K], of the tokens bias_tokens, int32 [R, K], K up to 8192:
+        x + bias (of several for one token the last);
       allowed, int32 [R, ceil(V / 32)] or more: bit t & 31 of word t >> 5 is set
         where token t is allowed; the others become -inf.
     tokens: the histories, int32 [R, L], of which the first lengths [R] (int32;
