@@ -32,12 +32,30 @@ namespace {
 static_assert(kLaChunk == TILE_ROWS);
 
 // Per-row values of a chunk, fp32 [4][32]: the running log2-decay as hi + lo,
-// exp(G) and exp(G_31 - G).
-constexpr int LS_H = 0, LS_L = 32, LS_GAM = 64, LS_LAST = 96, LS_FLOATS = 128;
+// exp(G) and exp(G_31 - G). Then the chunk's decay exp(G_31) as the state takes it: {1, d}
+// where it is 1 + d in [1/2, 2], the state becoming S + d S, else {p, 0}, p S.
+constexpr int LS_H = 0, LS_L = 32, LS_GAM = 64, LS_LAST = 96, LS_STEP = 128, LS_FLOATS = 132;
 
+constexpr double LN2 = 0.6931471805599453;
+// e^y - 1 for |y| <= ln 2, its series up to y^10 / 10! (1e-8 of the value is left out).
+__device__ __forceinline__ float expm1_small(float y) {
+    constexpr float c[9] = {1.f / 3628800, 1.f / 362880, 1.f / 40320, 1.f / 5040, 1.f / 720,
+                            1.f / 120,     1.f / 24,     1.f / 6,     1.f / 2};
+    float q = c[0];
+#pragma unroll
+    for (int i = 1; i < 9; ++i) q = __builtin_fmaf(q, y, c[i]);
+    return __builtin_fmaf(y * y, q, y);
+}
+
+// One fp32 number for a decay near 1 is off by up to 2^-25, and with a fixed
+// log-decay by the same in every chunk that the state remembers: 2048 chunks of
+// -1e-6, -1e-5 and -3e-5 a token left the state 1e-5, 9e-6 and 2e-5 off. d is off by
+// 2^-23 of what the chunk forgets instead, whatever the number of chunks.
+//
 // One wavefront: x = the log-decay of row lane & 31, after the log2-decay of the
 // tokens behind the chunk, which the last values get in addition. Returns the
-// chunk's log2-decay.
+// chunk's log2-decay. {p, d} go with outputs alone.
+template <bool OUT>
 __device__ __forceinline__ double row_scan(float x, double after, int lane, float* gs) {
     const int r = lane & 31;
     x *= LOG2E;
@@ -54,6 +72,11 @@ __device__ __forceinline__ double row_scan(float x, double after, int lane, floa
         gs[LS_L + r] = (float)(G - (double)hi);
         gs[LS_GAM + r] = exp2_hw(hi);
         gs[LS_LAST + r] = exp2_hw((float)(all - G + after));
+    }
+    if (OUT && lane == 31) {
+        const bool near = all >= -1.0 && all <= 1.0;
+        gs[LS_STEP] = near ? 1.f : exp2_hw(hi);
+        gs[LS_STEP + 1] = near ? expm1_small((float)(all * LN2)) : 0.f;
     }
     return all;
 }
@@ -234,7 +257,7 @@ __device__ __forceinline__ void produce(const Work& w, Lds<OUT>& lds, int lane) 
                     end = i + 2;
                     lds.stop = end;
                 } else {
-                    const double all = row_scan(lds.g[rg.at[2]][lane & 31], after, lane, lds.gs[gs.at[2]]);
+                    const double all = row_scan<OUT>(lds.g[rg.at[2]][lane & 31], after, lane, lds.gs[gs.at[2]]);
                     if constexpr (!OUT) after += all;
                 }
             }
@@ -366,11 +389,12 @@ __global__ __launch_bounds__(kLaThreads) void la_prefill(LaArgs a) {
 #pragma unroll
         for (int a = 0; a < 4; ++a) last[a] = *(const f32x4*)(row + LS_LAST + 8 * a + 4 * h);
     };
-    float gam_all, gam_row = 0.f;
+    u32x2 step = {0, 0};
+    float gam_row = 0.f;
     int n_steps = n_chunks;
     auto fetch_gam = [&](const float* row) __attribute__((always_inline)) {
         if constexpr (OUT) {
-            gam_all = row[LS_GAM + 31];
+            step = *(const u32x2*)(row + LS_STEP);
             gam_row = a.scale * row[LS_GAM + (lane & 31)];
         } else {
             n_steps = lds.stop;
@@ -401,13 +425,14 @@ __global__ __launch_bounds__(kLaThreads) void la_prefill(LaArgs a) {
     }
     counted_wait();
     for (int i = 0; i < (OUT ? n_chunks : __builtin_amdgcn_readfirstlane(n_steps)); ++i) {
-        const float gc = OUT ? gam_all : 1.f, gm = gam_row;
+        const float p = __uint_as_float(__builtin_amdgcn_readfirstlane(step.x));
+        const float d = __uint_as_float(__builtin_amdgcn_readfirstlane(step.y)), gm = gam_row;
         const u32x4 v0 = vw[0], v1 = vw[1];
         u32x4 ah[2], al[2], sb[2];
         f32x16 o = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
         if constexpr (OUT) pack_rows(S[0], sb);
         sched_fence();
-        // o = S Q, then S decays. A product of the matrix unit takes 32 cycles and leaves room for some five vector
+        // o = S Q. A product of the matrix unit takes 32 cycles and leaves room for some five vector
         // instructions, so they are issued in turn, with the LDS loads of what comes next.
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
@@ -429,9 +454,18 @@ __global__ __launch_bounds__(kLaThreads) void la_prefill(LaArgs a) {
                 sb[0] = after[0];
                 sb[1] = after[1];
             }
-            if constexpr (OUT) S[t] = gc * S[t];
             sched_fence();
         }
+        // (One of the two at most. Branches round each tile, or one with two sides, cost registers for copies of S.)
+        if (OUT && p != 1.f) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) S[t] = p * S[t];
+        }
+        if (OUT && d != 0.f) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) S[t] = __builtin_elementwise_fma(f32x16(d), S[t], S[t]);
+        }
+        sched_fence();
         // S += K^T (weighted V), beside the weighting for the next chunk
         Split3 next;
         f32x16 x;

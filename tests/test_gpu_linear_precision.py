@@ -1,0 +1,79 @@
+"""GPU tests of how far the states and outputs of linear attention may be from the
+exact ones, where a coarser arithmetic than the stated one would show: long
+sequences with slow decays, decays without new tokens, few tokens alone.
+
+The exact values are closed sums in 64 bits: S = sum over t of e^(decay behind t) k_t v_t^T."""
+import math
+
+import pytest
+import torch
+
+import kda_chunked_delta_amd as kda
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+D = 128
+
+
+def tokens(T, H, seed):
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+    return [torch.randn(T, H, D, generator=gen, device=DEV, dtype=torch.bfloat16) for _ in range(3)]
+
+
+def end_state(k, v, g):
+    """The state after all tokens, from zero, with one log-decay per head."""
+    T = k.shape[0]
+    behind = torch.arange(T - 1, -1, -1, device=DEV).double()
+    return torch.stack([(torch.exp(g[h].double() * behind)[:, None] * k[:, h].double()).t().contiguous()
+                        @ v[:, h].double() for h in range(k.shape[1])])
+
+
+# A decay per token and how far the state may be off as a whole, as a factor: the fp32
+# sums round it without a preferred sign, 16384 elements of it, which leaves 3e-8; the
+# weights of the tokens and the decay of a chunk are exponentials, off by 2^-23, of a
+# log-decay that is rounded to 2^-24, each counting once whatever the length: 5e-7 in all.
+# A state that decays by a few steps of its last bit per chunk (4e-8 a token: 11 to 21 of
+# them) is rounded to whole ones, which favours one sign by at most 1/8 of a step in
+# those: 2048 times 1e-9, of which a growing state remembers half.
+SLOW = [(-4e-8, 2e-6), (-1e-6, 5e-7), (-1e-5, 5e-7), (-3e-5, 5e-7), (-3e-4, 5e-7)]
+
+
+def slow_decays(plan_args, T=65536):
+    q, k, v = tokens(T, len(SLOW), seed=1)
+    g = torch.tensor([x for x, _ in SLOW], device=DEV)
+    plan = kda.plan_linear_attention([0, T], len(SLOW), *plan_args, device=DEV)
+    _, s = kda.linear_attention_prefill(q, k, v, g, cu_seqlens=[0, T], plan=plan, output_final_state=True)
+    want = end_state(k, v, g)
+    err = s[0].double() - want
+    for h, (x, most) in enumerate(SLOW):
+        norm = want[h].norm()
+        off, gain = (err[h].norm() / norm).item(), ((err[h] * want[h]).sum() / norm.square()).item()
+        print("  %8.0e a token: off %.2e, as a factor %+.2e" % (x, off, gain), flush=True)
+        # seven roundings of each element a chunk, at most 2^-24 of it and 2^-24 / sqrt(3) in the
+        # mean, over 2048 chunks of a state that grows with their root: 2.9e-6, and its factor
+        assert off <= 4e-6 and abs(gain) <= most, x
+
+
+def test_slow_decays_of_long_sequences():
+    slow_decays((False,))
+
+
+# The decay of a chunk of 32 tokens on both sides of 1/2, of 1 and of 2, and zero.
+@pytest.mark.parametrize("of_chunk", [0.49, 0.4999, 0.5, 0.5001, 0.51, 0.75, 0.999, 1.0, 1.001, 1.5, 1.999, 2.0, 2.001,
+                                      2.1, 1e-9, 0.0])
+def test_decays_without_new_tokens(of_chunk):
+    T = 32 * 12 + 7
+    q, k, v = tokens(T, 2, seed=2)
+    v.zero_()
+    g = torch.full((2,), math.log(of_chunk) / 32 if of_chunk else -math.inf, device=DEV)
+    s0 = torch.randn(1, 2, D, D, device=DEV)
+    _, s = kda.linear_attention_prefill(q, k, v, g, initial_state=s0, output_final_state=True, use_intracard_cp=False)
+    total = (g.double() * T)[None, :, None, None]
+    want = torch.exp(total) * s0.double()
+    # 13 chunks: an exponential (2^-23) and a rounding (2^-24) each; the log-decay is rounded to 2^-24 twice
+    tol = 13 * 1.5 * 2.0 ** -23 + total.abs().max().item() * 2.0 ** -23 if of_chunk else 0.0
+    off = (s.double() - want).abs()
+    if of_chunk != 1e-9:  # whose twelfth power is zero in 32 bits
+        assert (off <= tol * want.abs() + 1e-45).all()
+    else:
+        assert not s.any()
