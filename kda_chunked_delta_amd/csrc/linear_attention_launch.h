@@ -27,7 +27,7 @@ enum : int32_t { LA_NONE = -1, LA_FINAL = -2 };
 
 // The segments 0 .. n - 1 of one sequence. Slot slot0 + s is to hold the state
 // before segment s; before the merge, slot slot0 + s + 1 holds the end state of
-// segment s from zero and that slot's decay e^(sum of g over segment s).
+// segment s from zero and that slot's decay the sum of g over segment s, times log2(e).
 struct LaMerge {
     int32_t seq;
     int32_t n;
@@ -47,7 +47,7 @@ struct LaArgs {
     const void* s0;      // may be null: zero initial states
     void* sT;            // may be null
     float* slots;        // [n_slots][H][128][128]
-    float* decays;       // [n_slots][H]
+    float* decays;       // [n_slots][H], logarithms to base 2
     uint16_t* out;
     float scale;
     int32_t g_fixed, state_bf16;

@@ -58,6 +58,12 @@ def test_slow_decays_of_long_sequences():
     slow_decays((False,))
 
 
+@pytest.mark.parametrize("seg", [0, 1, 8])
+def test_slow_decays_of_segments(seg):
+    """Up to 2048 of them: the merge rounds a state once per segment, the decay between two counts like a chunk's."""
+    slow_decays((True, seg))
+
+
 # The decay of a chunk of 32 tokens on both sides of 1/2, of 1 and of 2, and zero.
 @pytest.mark.parametrize("of_chunk", [0.49, 0.4999, 0.5, 0.5001, 0.51, 0.75, 0.999, 1.0, 1.001, 1.5, 1.999, 2.0, 2.001,
                                       2.1, 1e-9, 0.0])
