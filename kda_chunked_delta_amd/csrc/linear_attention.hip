@@ -531,8 +531,10 @@ __global__ __launch_bounds__(kLaThreads) void la_prefill(LaArgs a) {
 // which holds the end state of segment s from zero, is added the decayed slot s. The
 // decays come as logarithms, and one near 1 is applied as in a chunk: its error does not
 // add up over the segments (2048 of one chunk, -4e-8 a token: 4e-5 of the state before).
-// One thread per four elements of a state; the loads of DEEP segments are in
-// flight together: 32 segments of 8 heads (32 MiB) take 8 us.
+// The others are applied as two roots, for what a state that has grown keeps of them below
+// 2^-126.
+// One thread per four elements of a state; the loads of DEEP segments are in flight
+// while the DEEP before are added: 64 segments of 4 heads (16 MiB) take 10 us.
 constexpr int DEEP = 8;
 static_assert(kLaMergeTiles * kLaMergeThreads * 4 == D * D);
 __global__ __launch_bounds__(kLaMergeThreads) void la_merge(LaMergeArgs a) {
@@ -540,37 +542,62 @@ __global__ __launch_bounds__(kLaMergeThreads) void la_merge(LaMergeArgs a) {
     const LaMerge it = a.items[ih / a.H];
     const int at = (tile * kLaMergeThreads + threadIdx.x) * 4;
     const int64_t own = ((int64_t)it.seq * a.H + hd) * (D * D) + at;
+    float* const first = a.slots + ((int64_t)it.slot0 * a.H + hd) * (D * D) + at;
+    const int64_t step = (int64_t)a.H * (D * D);
+    const int lane = threadIdx.x & 63;
+    // A segment of 64 per lane: its log2-decay (behind the end, the last one's again).
+    auto load_x = [&](int s) { return a.decays[(int64_t)(it.slot0 + (s < it.n ? s : it.n - 1)) * a.H + hd]; };
+    // The states of DEEP segments from s0 on, likewise.
+    auto load = [&](int s0, f32x4 (&b)[DEEP]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < DEEP; ++j) b[j] = *(const f32x4*)(first + (s0 + j < it.n ? s0 + j : it.n - 1) * step);
+    };
+    float x = load_x(1 + lane);
+    f32x4 b[DEEP];
+    load(1, b);
     f32x4 c = {0.f, 0.f, 0.f, 0.f};
     if (a.s0 && a.state_bf16) {
-        const u32x2 x = *(const u32x2*)((const uint16_t*)a.s0 + own);
-        c = f32x4{bf16_lo(x.x), bf16_hi(x.x), bf16_lo(x.y), bf16_hi(x.y)};
+        const u32x2 y = *(const u32x2*)((const uint16_t*)a.s0 + own);
+        c = f32x4{bf16_lo(y.x), bf16_hi(y.x), bf16_lo(y.y), bf16_hi(y.y)};
     } else if (a.s0) {
         c = *(const f32x4*)((const float*)a.s0 + own);
     }
-    auto slot = [&](int s) { return ((int64_t)(it.slot0 + s) * a.H + hd); };
-    *(f32x4*)(a.slots + slot(0) * (D * D) + at) = c;
-    for (int s0 = 1; s0 < it.n; s0 += DEEP) {
-        f32x4 b[DEEP];
-        float x[DEEP];  // log2-decays
+    *(f32x4*)first = c;
+    float lane_d = 0.f, lane_p = 0.f;
+    uint64_t nears = 0;
+    auto add = [&](int s0, bool all) __attribute__((always_inline)) {
+        const int from = (s0 - 1) & 63;
+        if (from == 0) {  // d of each lane's segment, and what c is multiplied with before
+            if (s0 > 1) x = load_x(s0 + lane);
+            const bool near = x >= -1.f && x <= 1.f;
+            const float half = exp2_hw(0.5f * x);
+            lane_d = near ? expm1_small(x * (float)LN2) : half;
+            lane_p = near ? 1.f : half;
+            nears = __builtin_amdgcn_ballot_w64(near);
+        }
 #pragma unroll
-        for (int j = 0; j < DEEP; ++j)
-            if (s0 + j < it.n) {
-                b[j] = *(const f32x4*)(a.slots + slot(s0 + j) * (D * D) + at);
-                x[j] = a.decays[slot(s0 + j)];
+        for (int j = 0; j < DEEP; ++j) {
+            const float d = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lane_d), from + j));
+            const float p = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lane_p), from + j));
+            const bool near = nears >> (from + j) & 1;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float y = __builtin_fmaf(d, p * c[e], b[j][e]);
+                c[e] = near ? c[e] + y : y;
             }
+            if (all || s0 + j < it.n) *(f32x4*)(first + (s0 + j) * step) = c;
+        }
+    };
+    int s0 = 1;
+    for (; s0 + DEEP < it.n; s0 += DEEP) {
+        f32x4 next[DEEP];
+        load(s0 + DEEP, next);
+        sched_fence();
+        add(s0, true);
 #pragma unroll
-        for (int j = 0; j < DEEP; ++j)
-            if (s0 + j < it.n) {
-                const bool near = x[j] >= -1.f && x[j] <= 1.f;
-                const float d = near ? expm1_small(x[j] * (float)LN2) : exp2_hw(x[j]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float y = __builtin_fmaf(d, c[e], b[j][e]);
-                    c[e] = near ? c[e] + y : y;
-                }
-                *(f32x4*)(a.slots + slot(s0 + j) * (D * D) + at) = c;
-            }
+        for (int j = 0; j < DEEP; ++j) b[j] = next[j];
     }
+    add(s0, false);
 }
 
 // Decode. With S the state before a token and gam = exp(g), for value column j:

@@ -83,3 +83,18 @@ def test_decays_without_new_tokens(of_chunk):
         assert (off <= tol * want.abs() + 1e-45).all()
     else:
         assert not s.any()
+
+
+def test_a_decay_between_segments_below_the_smallest_fp32_number():
+    """A state that has grown keeps a part of such a decay: e^80 of it, e^-96 and e^40 in a row, by segments."""
+    T = 192
+    q, k, v = tokens(3 * T, 1, seed=5)
+    v[T:] = 0
+    g = torch.empty(3 * T, 1, device=DEV)
+    g[:T], g[T:2 * T], g[2 * T:] = 80 / T, -96 / T, 40 / T
+    behind = g.double().flip(0).cumsum(0).flip(0) - g.double()
+    want = (torch.exp(behind) * k[:, 0].double()).t().contiguous() @ v[:, 0].double()
+    plan = kda.plan_linear_attention([0, 3 * T], 1, True, 6, device=DEV)
+    _, s = kda.linear_attention_prefill(q, k, v, g, cu_seqlens=[0, 3 * T], plan=plan, output_final_state=True)
+    # log-decays of 216 in all, rounded as such, as multiples of log2(e) and to sums, 2^-24 each
+    assert (s[0, 0].double() - want).norm() <= 216 * 3 * 2.0 ** -24 * want.norm()
