@@ -163,7 +163,8 @@ __device__ __forceinline__ void unrolled(F f) {
 // Without OUT (a segment's end state from zero) the chunks are taken from the
 // last to the first, V weighted by the decay up to the segment's end: the state
 // is never scaled, and the workgroup stops where that decay is zero in fp32
-// (below 2^-160), after a few chunks of a head that forgets fast.
+// (below 2^-160), after a few chunks of a head that forgets fast. Not where a
+// log-decay before is above zero, which could bring earlier tokens back, or NaN.
 // Ring slots: the tiles AHEAD + 1 chunks, A and the output 2, the row values 3.
 //
 // Bound by memory where every compute unit is at work: 4.65 to 4.95 TB/s of q, k, v
@@ -208,6 +209,24 @@ struct Work {
     float* decay;  // without OUT: gets the log2-decay over the unit's tokens
 };
 
+// One wavefront: whether a log-decay of the unit's first n > 0 tokens is not at most 0.
+__device__ __forceinline__ bool grows(const Work& w, int n, int lane) {
+    constexpr int AT_ONCE = 8;  // loads in flight together
+    if (w.st_g == 0) n = 1;
+    bool found = false;
+    for (int t0 = 0; t0 < n; t0 += 64 * AT_ONCE) {
+        float x[AT_ONCE];
+#pragma unroll
+        for (int j = 0; j < AT_ONCE; ++j) {
+            const int t = t0 + 64 * j + lane;
+            x[j] = *(const float*)((const uint8_t*)w.g + (size_t)(t < n ? t : n - 1) * w.st_g);
+        }
+#pragma unroll
+        for (int j = 0; j < AT_ONCE; ++j) found |= !(x[j] <= 0.f);
+    }
+    return __builtin_amdgcn_ballot_w64(found) != 0;
+}
+
 template <int ROLE, bool OUT, bool NT>
 __device__ __forceinline__ void produce(const Work& w, Lds<OUT>& lds, int lane) {
     Ring<N_TILE> tile;
@@ -234,7 +253,8 @@ __device__ __forceinline__ void produce(const Work& w, Lds<OUT>& lds, int lane) 
                                                    NT ? 2 : 0);
         }
     };
-    double after = 0.0;  // ROLE 3 without OUT: the log2-decay of the chunks scanned
+    double after = 0.0;    // ROLE 3 without OUT: the log2-decay of the chunks scanned
+    bool to_start = false;  // and whether those before have to be scanned whatever it is
     int end = w.n_chunks;
     if constexpr (ROLE == 3 && !OUT) lds.stop = end;
     // ring position j is step i + j
@@ -253,7 +273,9 @@ __device__ __forceinline__ void produce(const Work& w, Lds<OUT>& lds, int lane) 
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
                 rsrc, (__attribute__((address_space(3))) void*)lds.g[rg.at[AHEAD + 1]], 4, (int)off, 0, 0, 0);
             if (i + 2 >= 0 && i + 2 < end) {
-                if (!OUT && after <= LOG2_FLOOR) {
+                const bool gone = !OUT && __builtin_amdgcn_ballot_w64(after <= LOG2_FLOOR) != 0 && !to_start;
+                if (__builtin_expect(gone, 0)) to_start = grows(w, (place(i + 2) + 1) * TILE_ROWS, lane);
+                if (gone && !to_start) {
                     end = i + 2;
                     lds.stop = end;
                 } else {

@@ -98,3 +98,43 @@ def test_a_decay_between_segments_below_the_smallest_fp32_number():
     _, s = kda.linear_attention_prefill(q, k, v, g, cu_seqlens=[0, 3 * T], plan=plan, output_final_state=True)
     # log-decays of 216 in all, rounded as such, as multiples of log2(e) and to sums, 2^-24 each
     assert (s[0, 0].double() - want).norm() <= 216 * 3 * 2.0 ** -24 * want.norm()
+
+
+# ---------------------------------------------------------------------------
+# segments whose early tokens come back
+# ---------------------------------------------------------------------------
+def growing(T=384):
+    """Segments of 384 tokens, by chunks: a decay of e^-115 over the last four, growth of e^77 before and of e^38
+    in what follows them. Only the tokens before the decay have values, so that all of the state passes it."""
+    q, k, v = tokens(3 * T, 2, seed=3)
+    g = torch.zeros(3 * T, 2, device=DEV)
+    g[:256], g[256:384], g[384:512] = 0.3, -0.9, 0.3
+    g[:, 1] *= 0.5
+    v[256:] = 0
+    return q, k, v, g
+
+
+def test_growth_before_a_strong_decay_in_a_segment():
+    q, k, v, g = growing()
+    behind = g.double().flip(0).cumsum(0).flip(0) - g.double()
+    want = torch.stack([(torch.exp(behind[:, h])[:, None] * k[:, h].double()).t().contiguous() @ v[:, h].double()
+                        for h in range(2)])
+    for mode, seg in ((False, 0), (True, 12), (True, 6)):
+        plan = kda.plan_linear_attention([0, len(q)], 2, mode, seg, device=DEV)
+        o, s = kda.linear_attention_prefill(q, k, v, g, cu_seqlens=[0, len(q)], plan=plan, output_final_state=True)
+        off = ((s[0].double() - want).norm(dim=(1, 2)) / want.norm(dim=(1, 2))).tolist()
+        print("  segments of %d chunks: off %.2e %.2e" % (seg, *off), flush=True)
+        # log-decays of 230 in all, rounded as such (2^-24), as multiples of log2(e) (2^-24) and to sums (2^-24)
+        assert max(off) <= 230 * 3 * 2.0 ** -24, (seg, off)
+
+
+@pytest.mark.parametrize("seg", [0, 12])
+def test_a_log_decay_that_is_nan_reaches_the_end_from_everywhere(seg):
+    q, k, v = tokens(1200, 2, seed=4)
+    g = torch.full((1200, 2), -2.0, device=DEV)  # a segment's end state is that of its last few chunks
+    for at in (3, 500, 1199):
+        x = g.clone()
+        x[at, 1] = math.nan
+        plan = kda.plan_linear_attention([0, 1200], 2, seg > 0, seg, device=DEV)
+        _, s = kda.linear_attention_prefill(q, k, v, x, cu_seqlens=[0, 1200], plan=plan, output_final_state=True)
+        assert torch.isfinite(s[0, 0]).all() and s[0, 1].isnan().all(), at
