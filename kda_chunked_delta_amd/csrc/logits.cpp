@@ -1,7 +1,5 @@
 // Host side of the processing of logits: argument checks and dispatch of
 // logits.hip behind the C ABI of include/kda.h.
-#include <algorithm>
-
 #include "kda_internal.h"
 #include "logits_launch.h"
 
@@ -19,26 +17,6 @@ struct Buffer {
 // Bytes from the first row's start to the last row's end.
 size_t extent(int64_t rows, int64_t stride, int64_t n, size_t size) {
     return rows > 0 && n > 0 ? (size_t)((rows - 1) * stride + n) * size : 0;
-}
-
-// What a workgroup takes of a row: 8192 logits, or 2048 where that leaves the
-// chip with fewer than two workgroups per compute unit. With lists, which every
-// workgroup of a row goes through, 16384 or 4096; 8192 in place of 16384 where
-// words of 32 bits, or the room for a history of more than 4096 tokens, would
-// leave a compute unit fewer than four workgroups (40 KiB of LDS each). Measured
-// for 256 rows of 131072, histories of 4096 tokens: 37 us, 39 with 8192; of 8192
-// tokens (fp32): 92 with 16384, 82 with 8192.
-constexpr int32_t kSmallest = 2048;
-void split(LogitsArgs* a) {
-    const kda_logits& x = a->x;
-    a->lists = !x.tokens && !x.n_bias ? 0 : x.max_tokens < kLogitsShort ? 1 : 2;
-    a->threads = a->lists ? kLogitsListThreads : kLogitsThreads;
-    const int32_t large = a->lists == 1 && x.max_tokens <= 4096 ? 16384 : 8192;
-    const int32_t small = a->lists ? 2 * kSmallest : kSmallest;
-    a->chunk = (int64_t)x.rows * ((x.vocab + large - 1) / large) >= 512 ? large : small;
-    a->splits = (x.vocab + a->chunk - 1) / a->chunk;
-    const int32_t listed = x.tokens ? std::min(a->chunk, x.max_tokens) : 0;
-    a->lds = a->chunk * (a->lists == 1 ? 2 : 4) + (listed * 2 + 15) / 16 * 16;
 }
 
 }  // namespace
@@ -73,7 +51,7 @@ kda_status kda_logits_process_validate(const kda_logits* x) {
         x->allowed_stride > most)
         return fail(KDA_ERR_INVALID, "%s: strides must be at most 2^40", who);
     if (!x->tokens && x->max_tokens > 0) return fail(KDA_ERR_INVALID, "%s: tokens is NULL", who);
-    const int64_t splits = ((int64_t)x->vocab + 2 * kSmallest - 1) / (2 * kSmallest);
+    const int64_t splits = ((int64_t)x->vocab + 2 * kLogitsSmallest - 1) / (2 * kLogitsSmallest);
     if (!launchable(x->rows * splits, kLogitsListThreads))
         return fail(KDA_ERR_INVALID, "%s: rows * vocab too large", who);
     if (x->rows == 0) return KDA_OK;
@@ -114,7 +92,7 @@ kda_status kda_logits_process(kda_ctx* ctx, const kda_logits* x, hipStream_t str
     // a history that no penalty asks for is not looked at
     if (a.x.max_tokens == 0 || !(a.x.repetition || a.x.frequency || a.x.presence)) a.x.tokens = nullptr;
     if (a.x.logits == a.x.out && !a.x.tokens && !a.x.n_bias && !a.x.allowed) return KDA_OK;  // nothing changes
-    split(&a);
+    split_logits(&a);
     std::lock_guard<std::mutex> lk(ctx->mu);
     DeviceScope scope;
     hipError_t e = scope.enter(ctx->device);

@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "kda.h"
 
 namespace kda {
@@ -21,6 +23,26 @@ struct LogitsArgs {
     int32_t threads;
     int32_t lds;     // bytes
 };
+
+// What a workgroup takes of a row: 8192 logits, or 2048 where that leaves the
+// chip with fewer than two workgroups per compute unit. With lists, which every
+// workgroup of a row goes through, 16384 or 4096; 8192 in place of 16384 where
+// words of 32 bits, or the room for a history of more than 4096 tokens, would
+// leave a compute unit fewer than four workgroups (40 KiB of LDS each). Measured
+// for 256 rows of 131072, histories of 4096 tokens: 37 us, 39 with 8192; of 8192
+// tokens (fp32): 92 with 16384, 82 with 8192.
+constexpr int32_t kLogitsSmallest = 2048;
+inline void split_logits(LogitsArgs* a) {
+    const kda_logits& x = a->x;
+    a->lists = !x.tokens && !x.n_bias ? 0 : x.max_tokens < kLogitsShort ? 1 : 2;
+    a->threads = a->lists ? kLogitsListThreads : kLogitsThreads;
+    const int32_t large = a->lists == 1 && x.max_tokens <= 4096 ? 16384 : 8192;
+    const int32_t small = a->lists ? 2 * kLogitsSmallest : kLogitsSmallest;
+    a->chunk = (int64_t)x.rows * ((x.vocab - 1) / large + 1) >= 512 ? large : small;
+    a->splits = (x.vocab - 1) / a->chunk + 1;
+    const int32_t listed = x.tokens ? std::min(a->chunk, x.max_tokens) : 0;
+    a->lds = a->chunk * (a->lists == 1 ? 2 : 4) + (listed * 2 + 15) / 16 * 16;
+}
 
 hipError_t launch_logits(const LogitsArgs& a, hipStream_t s);
 
