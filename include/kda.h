@@ -677,8 +677,8 @@ kda_status kda_beam_select_validate(int32_t batch, int32_t beams, int32_t vocab,
  * logits' type. A logit that nothing applies to keeps its bits. Tokens outside
  * [0, vocab) in a list (-1 for padding) are skipped. A row whose mask allows
  * nothing becomes -inf. Pointers are device memory; each part may be left out
- * (NULL, or a count of 0). Rows are strides (in elements) apart; a stride of 0
- * gives all rows the same list or mask. */
+ * (NULL, or a count of 0). Rows are strides (in elements) apart, at most 2^40, and
+ * rows times one below 2^60; a stride of 0 gives all rows the same list or mask. */
 typedef struct {
     int32_t rows, vocab;
     kda_dtype dtype;               /* of logits and out */

@@ -46,7 +46,7 @@ kda_status kda_logits_process_validate(const kda_logits* x) {
         if (s.p && s.stride != 0 && s.stride < s.n)
             return fail(KDA_ERR_INVALID, "%s: %s must be 0 or at least a row's %lld entries (got %lld)", who, s.name,
                         (long long)s.n, (long long)s.stride);
-    const int64_t most = (int64_t)1 << 40;  // keeps the extents in 64 bits
+    const int64_t most = (int64_t)1 << 40;
     if (x->row_stride > most || x->out_stride > most || x->token_stride > most || x->bias_stride > most ||
         x->allowed_stride > most)
         return fail(KDA_ERR_INVALID, "%s: strides must be at most 2^40", who);
@@ -55,6 +55,12 @@ kda_status kda_logits_process_validate(const kda_logits* x) {
     if (!launchable(x->rows * splits, kLogitsListThreads))
         return fail(KDA_ERR_INVALID, "%s: rows * vocab too large", who);
     if (x->rows == 0) return KDA_OK;
+    // from the first row's start to the last one's end, 2^60 entries keep the bytes in 64 bits
+    for (const int64_t stride : {x->row_stride, x->out_stride, x->tokens ? x->token_stride : 0,
+                                 x->n_bias ? x->bias_stride : 0, x->allowed ? x->allowed_stride : 0})
+        if ((x->rows - 1) * (stride >> 20) >= (int64_t)1 << 40)
+            return fail(KDA_ERR_INVALID, "%s: rows * stride must be below 2^60 (got %d, %lld)", who, x->rows,
+                        (long long)stride);
     const size_t size = x->dtype == KDA_FP32 ? 4 : 2, R = (size_t)x->rows;
     if (!x->logits || !x->out) return fail(KDA_ERR_INVALID, "%s: %s is NULL", who, x->logits ? "out" : "logits");
     if (x->n_bias && (!x->bias || !x->bias_tokens))
