@@ -95,10 +95,8 @@ kda_status kda_logits_process(kda_ctx* ctx, const kda_logits* x, hipStream_t str
     if (st != KDA_OK || x->rows == 0) return st;
     LogitsArgs a{};
     a.x = *x;
-    // a history that no penalty asks for is not looked at
-    if (a.x.max_tokens == 0 || !(a.x.repetition || a.x.frequency || a.x.presence)) a.x.tokens = nullptr;
-    if (a.x.logits == a.x.out && !a.x.tokens && !a.x.n_bias && !a.x.allowed) return KDA_OK;  // nothing changes
     split_logits(&a);
+    if (a.x.logits == a.x.out && !a.x.tokens && !a.x.n_bias && !a.x.allowed) return KDA_OK;  // nothing changes
     std::lock_guard<std::mutex> lk(ctx->mu);
     DeviceScope scope;
     hipError_t e = scope.enter(ctx->device);

@@ -33,14 +33,17 @@ struct LogitsArgs {
 // tokens (fp32): 92 with 16384, 82 with 8192.
 constexpr int32_t kLogitsSmallest = 2048;
 inline void split_logits(LogitsArgs* a) {
-    const kda_logits& x = a->x;
+    kda_logits& x = a->x;
+    // a history that no penalty asks for is not looked at, and takes no room
+    if (!x.tokens || !(x.repetition || x.frequency || x.presence)) x.max_tokens = 0;
+    if (x.max_tokens == 0) x.tokens = nullptr;
     a->lists = !x.tokens && !x.n_bias ? 0 : x.max_tokens < kLogitsShort ? 1 : 2;
     a->threads = a->lists ? kLogitsListThreads : kLogitsThreads;
     const int32_t large = a->lists == 1 && x.max_tokens <= 4096 ? 16384 : 8192;
     const int32_t small = a->lists ? 2 * kLogitsSmallest : kLogitsSmallest;
     a->chunk = (int64_t)x.rows * ((x.vocab - 1) / large + 1) >= 512 ? large : small;
     a->splits = (x.vocab - 1) / a->chunk + 1;
-    const int32_t listed = x.tokens ? std::min(a->chunk, x.max_tokens) : 0;
+    const int32_t listed = std::min(a->chunk, x.max_tokens);
     a->lds = a->chunk * (a->lists == 1 ? 2 : 4) + (listed * 2 + 15) / 16 * 16;
 }
 

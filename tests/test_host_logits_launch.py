@@ -70,3 +70,12 @@ def test_the_chunks_of_a_row_cover_it(split, rows, vocab):
         assert 0 < a["lds"] <= 65536, (case, a)
         # many workgroups at the largest chunk are not cut finer
         assert rows * -(-vocab // 16384) < 512 or a["chunk"] >= 8192, (case, a)
+
+
+@pytest.mark.parametrize("n_bias", [0, 1, 64])
+@pytest.mark.parametrize("length", [1, 4096, 4097, 1 << 14, (1 << 30) - 1])
+def test_a_history_without_penalties_takes_no_room(split, n_bias, length):
+    """It is not looked at, so the call is cut as one without it."""
+    sizes = dict(rows=256, vocab=131072, n_bias=n_bias)
+    without, with_it = split([sizes, dict(sizes, tokens=1, max_tokens=length, penalty=0)])
+    assert with_it == without
