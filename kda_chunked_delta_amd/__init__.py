@@ -205,8 +205,18 @@ def _cp_mode(use_intracard_cp):
     raise ValueError("use_intracard_cp must be 'auto', True or False (got %r)" % (use_intracard_cp,))
 
 
+def _i32(name, x):
+    """x as an int that the C ABI's 32 bits hold (ctypes would cut it to them)."""
+    x = int(x)
+    if not -2**31 <= x < 2**31:
+        raise ValueError("%s must be below 2^31 (got %d)" % (name, x))
+    return x
+
+
 def _cu_array(cu):
     cu = [int(x) for x in cu]
+    for x in (min(cu), max(cu)) if cu else ():
+        _i32("cu_seqlens", x)
     return (ctypes.c_int32 * len(cu))(*cu), len(cu) - 1
 
 
@@ -774,8 +784,9 @@ def plan_linear_attention(cu_seqlens, H, use_intracard_cp="auto", seg_chunks=0, 
     ctx = context(device)
     arr, n = _cu_array(cu_seqlens)
     h = ctypes.c_void_p()
-    _check(lib().kda_plan_linear_attention(ctx.handle, arr, n, int(H), D, D, _cp_mode(use_intracard_cp),
-                                           int(seg_chunks), ctypes.byref(h)), "kda_plan_linear_attention")
+    _check(lib().kda_plan_linear_attention(ctx.handle, arr, n, _i32("H", H), D, D, _cp_mode(use_intracard_cp),
+                                           _i32("seg_chunks", seg_chunks), ctypes.byref(h)),
+           "kda_plan_linear_attention")
     return Plan(h, cu_seqlens, ctx.device)
 
 
@@ -783,8 +794,9 @@ def plan_linear_attention_host(cu_seqlens, H, n_cus, use_intracard_cp="auto", se
     """The same for an explicit CU count (inspection; no GPU needed)."""
     arr, n = _cu_array(cu_seqlens)
     h = ctypes.c_void_p()
-    _check(lib().kda_plan_linear_attention_host(int(n_cus), arr, n, int(H), D, D, _cp_mode(use_intracard_cp),
-                                                int(seg_chunks), ctypes.byref(h)), "kda_plan_linear_attention_host")
+    _check(lib().kda_plan_linear_attention_host(_i32("n_cus", n_cus), arr, n, _i32("H", H), D, D,
+                                                _cp_mode(use_intracard_cp), _i32("seg_chunks", seg_chunks),
+                                                ctypes.byref(h)), "kda_plan_linear_attention_host")
     return Plan(h, cu_seqlens)
 
 
@@ -1065,6 +1077,8 @@ def _rows(name, t, dtype, lead, device):
         raise ValueError("%s must be a %s tensor [%s, n] on cuda:%d (got %s %s on %s)"
                          % (name, dtype, ", ".join(map(str, lead)), device, t.dtype, tuple(t.shape), t.device))
     n = shape[-1]
+    if n >> 31:
+        raise ValueError("the rows of %s must be below 2^31 (got %d)" % (name, n))
     if t.is_contiguous():
         return t.data_ptr(), n, n
     stride = t.stride()
@@ -1108,7 +1122,7 @@ def logits_process(logits, tokens=None, lengths=None, prompt_lengths=None, repet
     if V < 1:
         raise ValueError("logits have an empty vocabulary")
     a = Logits()
-    a.rows, a.vocab, a.dtype = lead.numel(), V, dtype
+    a.rows, a.vocab, a.dtype = _i32("the rows of logits", lead.numel()), V, dtype
     a.logits, _, a.row_stride = _rows("logits", logits, logits.dtype, lead, dev)
     if out is None:
         step = 32 if dtype == 0 else 64  # rows of whole 128-byte lines
