@@ -138,3 +138,50 @@ def test_a_log_decay_that_is_nan_reaches_the_end_from_everywhere(seg):
         plan = kda.plan_linear_attention([0, 1200], 2, seg > 0, seg, device=DEV)
         _, s = kda.linear_attention_prefill(q, k, v, x, cu_seqlens=[0, 1200], plan=plan, output_final_state=True)
         assert torch.isfinite(s[0, 0]).all() and s[0, 1].isnan().all(), at
+
+
+# ---------------------------------------------------------------------------
+# what the computed operands keep
+# ---------------------------------------------------------------------------
+def halves(x, n):
+    """The sum of x's first n bf16 parts, each the rounding of what the ones before leave."""
+    total = torch.zeros_like(x)
+    for _ in range(n):
+        total = total + (x - total).bfloat16().to(x.dtype)
+    return total
+
+
+@pytest.mark.parametrize("T,seg", [(32, 0), (23, 0), (64, 1), (96, 1)])
+def test_a_token_enters_a_state_with_all_its_bits(T, seg):
+    """In the norm: the weights are exponentials (2^-23) of log-decays below 1 that are rounded (2^-23), times v (2^-24),
+    in sums with six roundings a chunk, 2^-24 / sqrt(3) in the mean; the decay between chunks (2^-23) and its sum."""
+    g = torch.tensor([-0.003, -0.01, -0.007, -0.0301], device=DEV)
+    q, k, v = tokens(T, 4, seed=6)
+    plan = kda.plan_linear_attention([0, T], 4, seg > 0, seg, device=DEV)
+    _, s = kda.linear_attention_prefill(q, k, v, g, cu_seqlens=[0, T], plan=plan, output_final_state=True)
+    want = end_state(k, v, g)
+    tol = 7e-7
+    off = ((s[0].double() - want).norm(dim=(1, 2)) / want.norm(dim=(1, 2))).max().item()
+    # what two parts of the weighted v would leave, with everything else exact
+    w = torch.exp(g.double()[None] * torch.arange(T - 1, -1, -1, device=DEV).double()[:, None])[..., None] * v.double()
+    two = torch.stack([k[:, h].double().t().contiguous() @ halves(w, 2)[:, h] for h in range(4)])
+    coarse = ((two - want).norm(dim=(1, 2)) / want.norm(dim=(1, 2))).min().item()
+    print("  off %.2e, with two parts %.2e" % (off, coarse), flush=True)
+    assert off <= tol and coarse > 2 * tol
+
+
+@pytest.mark.parametrize("at", [0, 5, 15, 16, 20])
+def test_a_product_of_q_and_k_reaches_an_output_with_more_than_eight_bits(at):
+    """One key alone, so that an output row is one product times its v: a rounding of the product scales the row.
+    Rounding the row's 128 outputs looks like a factor of at most 2^-8 / sqrt(3) times sqrt(3 / 128) in the mean."""
+    T, H, scale = 32, 16, 0.7301
+    q, k, v = tokens(T, H, seed=7)
+    k[:at], k[at + 1:] = 0, 0
+    o, _ = kda.linear_attention_prefill(q, k, v, torch.zeros(H, device=DEV), scale=scale)
+    A = scale * (q.double() * k[at].double()).sum(-1)[at:]  # [tokens, H]
+    want = A[..., None] * v[at].double()
+    factor = lambda x: (((x - want) * want).sum(-1) / want.square().sum(-1)).square().mean().sqrt().item()
+    off, coarse = factor(o[at:].double()), factor((halves(A, 1)[..., None] * v[at].double()).bfloat16().double())
+    print("  off %.2e, with one part %.2e" % (off, coarse), flush=True)
+    assert not o[:at].any()
+    assert off <= 2.0 ** -8 / 128 ** 0.5 * 1.2 and coarse > 2 * 2.0 ** -8 / 128 ** 0.5
