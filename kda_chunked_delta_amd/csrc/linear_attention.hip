@@ -675,7 +675,10 @@ __global__ __launch_bounds__(kLaDecodeThreads) void la_decode(LaDecodeArgs a) {
         if (t + 1 < a.T) next = load(t + 1);
         const u32x4 (&k2)[2] = now.k, (&q2)[2] = now.q;
         const u32x2 vb = now.v;
-        const float gam = exp2_hw(now.g * LOG2E);
+        // the decay as one + d, the state's part of it rounded once: as in the prefill, its error near 1 does not
+        // add up over the tokens of a generation
+        const bool near = __builtin_fabsf(now.g) <= (float)LN2;
+        const float d = near ? expm1_small(now.g) : exp2_hw(now.g * LOG2E), one = near ? 1.f : 0.f, gam = one + d;
         float k[16], q[16], qk = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -692,7 +695,7 @@ __global__ __launch_bounds__(kLaDecodeThreads) void la_decode(LaDecodeArgs a) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 sb[j] = __builtin_fmaf(q[i], s[i][j], sb[j]);
-                s[i][j] = __builtin_fmaf(gam, s[i][j], k[i] * v[j]);
+                s[i][j] = __builtin_fmaf(one, s[i][j], __builtin_fmaf(d, s[i][j], k[i] * v[j]));
             }
         }
 #pragma unroll

@@ -185,3 +185,22 @@ def test_a_product_of_q_and_k_reaches_an_output_with_more_than_eight_bits(at):
     print("  off %.2e, with one part %.2e" % (off, coarse), flush=True)
     assert not o[:at].any()
     assert off <= 2.0 ** -8 / 128 ** 0.5 * 1.2 and coarse > 2 * 2.0 ** -8 / 128 ** 0.5
+
+
+def test_slow_decays_of_long_generations():
+    """A state is rounded once a token: 2^-24 / sqrt(3) in the mean over 4096 of them and a state that grows with
+    their root, 1.6e-6, and with no preferred sign but where it decays by a few steps of its last bit (17 at -1e-6:
+    1 / 8 of a step in those, half of 4096 times 7e-10)."""
+    T = 4096
+    decays = [(-1e-6, 2e-6), (-1e-5, 5e-7), (-3e-5, 5e-7), (-1e-4, 5e-7), (-1e-3, 5e-7)]
+    q, k, v = tokens(T, len(decays), seed=8)
+    g = torch.tensor([x for x, _ in decays], device=DEV)
+    s = torch.zeros(1, len(decays), D, D, device=DEV)
+    kda.linear_attention_decode(q[None], k[None], v[None], g, s)
+    want = end_state(k, v, g)
+    err = s[0].double() - want
+    for h, (x, most) in enumerate(decays):
+        norm = want[h].norm()
+        off, gain = (err[h].norm() / norm).item(), ((err[h] * want[h]).sum() / norm.square()).item()
+        print("  %8.0e a token: off %.2e, as a factor %+.2e" % (x, off, gain), flush=True)
+        assert off <= 3e-6 and abs(gain) <= most, x
