@@ -19,7 +19,7 @@ constexpr int32_t kMaxHeads = 1 << 17;  // 32 token rows of one tensor stay belo
 // units: what a chunk of a unit takes at least, with output and without, and at
 // what rate the whole chip moves the bytes of a chunk (32 KiB with output, 16
 // without); a launch beside its chunks; a segment's step of the merge.
-constexpr double kFullUs = 1.08, kPreUs = 0.82, kBytesPerUs = 5.0e6, kLaunchUs = 6.0, kMergeUs = 0.1;
+constexpr double kFullUs = 1.13, kPreUs = 0.82, kBytesPerUs = 5.0e6, kLaunchUs = 6.0, kMergeUs = 0.1;
 
 // A launch of units, H heads each: bound by the chain of the longest one, by
 // the workgroups that share a compute unit, or by memory.
