@@ -500,13 +500,19 @@ kda_status kda_gated_delta_decode_validate(int32_t n_seqs, int32_t n_tokens, int
  *   S_t = exp(g_t) S_{t-1} + k_t v_t^T,   o_t = scale * S_t^T q_t,
  * over the packed layouts and states of the gated delta rule, with a log-decay g
  * (g <= 0 expected; -inf forgets the state) per token and head, or one per head
- * for all tokens. In the prefill, sums are fp32 and what a token adds to the
- * state enters with all 24 bits of its mantissa: an fp32 state is within 1e-6 of
- * the exact one relative to its norm (3e-7 measured, plain fp32 arithmetic is within
- * about 2e-7). The copy of the state that an output reads is rounded to bf16 once,
- * as the output is. Decoding is fp32 throughout. All other inputs have to be
+ * for all tokens. In the prefill, sums are fp32, what a token adds to the
+ * state enters with all 24 bits of its mantissa, and the error of a decay does not
+ * add up: an fp32 state is as far from the exact one as its fp32 sums are, which
+ * grows with the root of the tokens that it remembers. Relative to its norm that is
+ * within 5e-7 for up to 1024 tokens, 2e-6 for 8192 and 5e-6 for 65536 (measured:
+ * 3e-7, 9e-7 and 4e-6, and a third of that where the plan cuts the sequence). The copy of the
+ * state that an output reads is rounded to bf16 once, as the output is. Decoding is
+ * fp32 throughout. Log-decays above 0 grow the state, and are followed as long as
+ * its values stay within fp32 in each chunk. All other inputs have to be
  * finite: a value that is not reaches the results of its own sequence and head from
- * its chunk of 32 tokens on, that is also of up to 31 tokens before it.
+ * its chunk of 32 tokens on, that is also of up to 31 tokens before it (one in v or a
+ * state: those of its own value column). Where a plan cuts the sequence, one in k or v
+ * does not reach later segments if the decay behind it in its own is below 2^-160.
  * ------------------------------------------------------------------------- */
 
 /* Build the plan of a packed batch for kda_linear_attention_prefill: as
@@ -516,7 +522,7 @@ kda_status kda_gated_delta_decode_validate(int32_t n_seqs, int32_t n_tokens, int
  * fp32. The plan is only accepted by kda_linear_attention_prefill, and the
  * inspection calls. A segment's tokens whose decay up to the segment's end is
  * below 2^-160 (zero in fp32) are left out of its end state, which makes segments
- * cheaper for heads that forget fast. */
+ * cheaper for heads that forget fast (unless a log-decay before them is above 0). */
 kda_status kda_plan_linear_attention(kda_ctx *ctx, const int32_t *cu_seqlens_host, int32_t n_seqs, int32_t H,
                                      int32_t dk, int32_t dv, kda_cp_mode mode, int32_t seg_chunks, kda_plan **out);
 

@@ -12,15 +12,26 @@
 // into the state, never q and k, which go to the matrix instructions as they
 // are in memory. What is computed in fp32 and then multiplied is rounded so:
 //   - diag(exp(G_31 - G)) V becomes the sum of three bf16 numbers, all 24 bits of
-//     its mantissa, since the state keeps its sum: one bf16 would leave 2^-9 of
-//     each token in an fp32 state, two 2^-18;
+//     its mantissa, since the state keeps its sum: one bf16 would leave up to 2^-8 of
+//     each token in an fp32 state, two 2^-17 (2e-6 of its norm). The third part costs
+//     7 to 8% (16 prompts of 2048 tokens and 64 heads 424 and 461 us);
 //   - A becomes a pair hi + lo (2^-17): a rounding of one of its few large values
-//     would reach a whole row of an output, and not average out;
+//     would reach a whole row of an output, and not average out (2 to 3%);
 //   - the copy of S that Q S multiplies becomes one bf16 (2^-8 at most of each
-//     value): a sum over its 128 channels reaches the output, which is bf16 itself.
+//     value). It is read and not kept: its rounding reaches one output, as a sum over
+//     128 channels that is rounded to bf16 itself, 1.7e-3 of its norm, and adds up to
+//     2.3e-3 with that. A pair would leave the 1.7e-3, for 16 more products a chunk:
+//     1.29 against 1.12 us with 8 workgroups, 522 against 453 us for the 16 prompts,
+//     195 against 169 for eight packed ones. (The gated delta rule reads its state into
+//     what it writes next, and takes the pair.)
 // All sums are fp32, the running sum of g is fp64 (differences of it are taken).
-// An fp32 state ends within 3e-7 of the exact one (its norm); plain fp32
-// arithmetic within 2e-7.
+// A decay near 1 is applied as its difference to 1, so that its error does not add up
+// over the chunks that a state remembers. What is left of an fp32 state's error is the
+// rounding of its sums, some seven a chunk without a preferred sign: 6e-8 of its norm
+// after 32 tokens, 3e-7 after 1024, 9e-7 after 8192, 2.6e-6 after 65536, with slow
+// decays, and a third of that in the segments of a plan. (A decay that is a few steps
+// of the state's last bit a chunk is rounded to whole ones: 3.7e-6 after 65536 tokens
+// of -1e-8.)
 #include "chunk_tiles.hpp"
 #include "linear_attention_launch.h"
 
@@ -167,21 +178,21 @@ __device__ __forceinline__ void unrolled(F f) {
 // log-decay before is above zero, which could bring earlier tokens back, or NaN.
 // Ring slots: the tiles AHEAD + 1 chunks, A and the output 2, the row values 3.
 //
-// Bound by memory where every compute unit is at work: 4.65 to 4.95 TB/s of q, k, v
-// and o, where a copy of 1 GiB reaches 5.15 (1.7 us a chunk for 256 workgroups; 16
-// prompts of 2048 tokens and 64 heads 435 to 461 us, 3 to 4% less without A's
-// second part). With fewer workgroups by the chain of chunks, 1.05 us each with 8
-// to 32 of them, and by what one compute unit has in flight, 28 GB/s, 1.18 us with
-// 128. The chain's 2400 cycles are 36 products of 32 cycles and some 200 vector instructions of 4 on each state wavefront, which
-// its SIMD issues one after the other, and those of the operand wavefront beside it.
+// Bound by memory where every compute unit is at work: 4.6 to 4.75 TB/s of q, k, v
+// and o, where a copy of 1 GiB reaches 5.15 (1.73 us a chunk for 256 workgroups; 16
+// prompts of 2048 tokens and 64 heads 453 to 465 us; at this load the clock falls, so
+// that products count too). With fewer workgroups by the chain of chunks, 1.10 us each
+// (1.12 with decays near 1) with 8 to 32 of them, 1.15 with 128. The chain's 2700
+// cycles are 40 products of 32 cycles (8 of S Q, 24 of K^T V, 4 of A V, 4 of V's rests)
+// and some 250 vector instructions of 4 on each state wavefront, which its SIMD issues
+// one after the other, and those of the operand wavefront beside it.
 // Steps that were measured, us a chunk with 8 workgroups: LDS loads next to their
 // use 1.24; loads, products and vector instructions issued in turn and a phase
 // ahead, A by three wavefronts instead of one 1.17; the state's wavefronts first on
-// their SIMD 1.06. Outputs as rows through LDS instead of 32 bytes per token and
-// wavefront: 457 to 430 us for the 16 prompts. Not better: 8 state wavefronts of 16
-// columns on 16x16x32 products (1.20 a chunk; every operand is read twice as often),
-// V in two parts instead of three (0.99 with 8 workgroups, no change at full load,
-// and 3e-6 of the state lost), 3 to 8 chunks of loads ahead, heads in the order of
+// their SIMD 1.06; decays near 1 as a difference 1.12. Outputs as rows through LDS
+// instead of 32 bytes per token and wavefront: 457 to 430 us for the 16 prompts. Not
+// better: 8 state wavefronts of 16 columns on 16x16x32 products (1.20 a chunk; every
+// operand is read twice as often), 3 to 8 chunks of loads ahead, heads in the order of
 // the XCDs.
 constexpr int AHEAD = 4;
 constexpr int N_TILE = AHEAD + 1, N_A = 2, N_O = 2, N_GS = 3, N_G = AHEAD + 2;
@@ -626,12 +637,13 @@ __global__ __launch_bounds__(kLaMergeThreads) void la_merge(LaMergeArgs a) {
 
 // Decode. With S the state before a token and gam = exp(g), for value column j:
 //   o_j = scale (gam sum_r q_r S_rj + (q . k) v_j),   S'_rj = gam S_rj + k_r v_j
+// with a gam in [1/2, 2] as 1 + d, S + (d S + k v) (256 sequences 192 us, 190 with the product).
 // One wavefront per (sequence, head, 32-column tile) keeps its part of the
 // state in registers over all T tokens: lane (rs, cg) = (lane >> 3, lane & 7)
 // owns rows 16rs .. + 15 of columns 4cg .. + 3, so a load instruction covers
 // eight whole 128-byte lines, the sums need three lane exchanges and the
 // kernel needs neither LDS nor a barrier. Bound by HBM: 256 sequences of 32 heads
-// take 188 us (5.7 TB/s); one sequence takes 4, the latency of the launch and of
+// take 190 to 193 us (5.6 TB/s); one sequence takes 4, the latency of the launch and of
 // one load after another.
 //
 // States beyond 128 MiB, half the last-level cache, are read and written with
@@ -677,8 +689,8 @@ __global__ __launch_bounds__(kLaDecodeThreads) void la_decode(LaDecodeArgs a) {
         if (t + 1 < a.T) next = load(t + 1);
         const u32x4 (&k2)[2] = now.k, (&q2)[2] = now.q;
         const u32x2 vb = now.v;
-        // the decay as one + d, the state's part of it rounded once: as in the prefill, its error near 1 does not
-        // add up over the tokens of a generation
+        // the decay as one + d: as in the prefill, the error of one near 1 does not add up, here over the tokens of a
+        // generation (4096 of -1e-6 left a state 3.4e-5 off, now 2.7e-6)
         const bool near = __builtin_fabsf(now.g) <= (float)LN2;
         const float d = near ? expm1_small(now.g) : exp2_hw(now.g * LOG2E), one = near ? 1.f : 0.f, gam = one + d;
         float k[16], q[16], qk = 0.f;
@@ -745,9 +757,9 @@ hipError_t run_la_prefill(const LaArgs& a, hipStream_t s) {
 hipError_t launch_la_prefill(const LaArgs& a, bool with_out, hipStream_t s) {
     if (a.n_units == 0) return hipSuccess;
     // What the last-level cache (256 MiB) cannot hold is streamed with the
-    // nontemporal hint: 440 and 424 us for 16 prompts of 2048 tokens and 64 heads
-    // (2 GiB), 190 and 178 for 65536 tokens of 8 heads. Not in the segments' pass,
-    // which leaves k and v to the second one (178 us, and 190 with the hint).
+    // nontemporal hint: 472 us without and 461 with it for 16 prompts of 2048 tokens and
+    // 64 heads (2 GiB), 191 and 187 for 65536 tokens of 8 heads. Not in the segments' pass,
+    // which leaves k and v to the second one (178 us, and 190 with the hint there, when measured).
     const bool nt = (size_t)a.Tt * (a.H + a.Hk) * (4 * D) > ((size_t)256 << 20);
     if (!with_out) return run_la_prefill<false, false>(a, s);
     return nt ? run_la_prefill<true, true>(a, s) : run_la_prefill<true, false>(a, s);

@@ -24,13 +24,13 @@ struct LogitsArgs {
     int32_t lds;     // bytes
 };
 
-// What a workgroup takes of a row: 8192 logits, or 2048 where that leaves the
-// chip with fewer than two workgroups per compute unit. With lists, which every
-// workgroup of a row goes through, 16384 or 4096; 8192 in place of 16384 where
-// words of 32 bits, or the room for a history of more than 4096 tokens, would
-// leave a compute unit fewer than four workgroups (40 KiB of LDS each). Measured
-// for 256 rows of 131072, histories of 4096 tokens: 37 us, 39 with 8192; of 8192
-// tokens (fp32): 92 with 16384, 82 with 8192.
+// What a workgroup takes of a row: 8192 logits, or 2048 where that leaves the 256
+// compute units with fewer than two workgroups each. With lists, which every
+// workgroup of a row goes through, 16384 or 4096. 8192 in place of 16384 with
+// words of 32 bits (64 KiB of LDS otherwise), and for a history of more than 4096
+// tokens, whose list takes the LDS of a third workgroup per compute unit (41 KiB each
+// with 4096 tokens, 49 with 8192, of 160): 256 rows of 131072 took 37 us with histories of
+// 4096 tokens, 39 with 8192 logits; with histories of 8192 tokens (fp32) 92, and 82.
 constexpr int32_t kLogitsSmallest = 2048;
 inline void split_logits(LogitsArgs* a) {
     kda_logits& x = a->x;
