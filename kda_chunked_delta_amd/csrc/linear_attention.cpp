@@ -17,8 +17,8 @@ constexpr int32_t kMaxHeads = 1 << 17;  // 32 token rows of one tensor stay belo
 
 // Cost model of a plan, microseconds on MI355X, fitted to launches of 8 to 1024
 // units: what a chunk of a unit takes at least, with output and without, and at
-// what rate the whole chip moves the bytes of a chunk (32 KiB with output, 16
-// without); a launch beside its chunks; a segment's step of the merge.
+// what rate the whole chip (256 compute units) moves the bytes of a chunk (32 KiB
+// with output, 16 without); a launch beside its chunks; a segment's step of the merge.
 constexpr double kFullUs = 1.13, kPreUs = 0.82, kBytesPerUs = 5.0e6, kLaunchUs = 6.0, kMergeUs = 0.1;
 
 // A launch of units, H heads each: bound by the chain of the longest one, by
